@@ -8,10 +8,14 @@ not built, every call raises.
 Names and keyword arguments follow mlx-arsenal's ``mlx_arsenal.diffusion``
 functions ("dLLM block decoding", "What mlx-arsenal ships"): token_stats,
 threshold_transfer, topk_transfer, factor_transfer, entropy_bound_transfer,
-edit_transfer, transfer_schedule, block_ranges, block_causal_mask.
+edit_transfer, transfer_schedule, block_ranges, block_causal_mask.  Around the
+step: token_logprobs (scores of given tokens, differentiable), and the 8-bit
+key/value cache of block decoding (KVCache, kv_write, kv_read, block_attention,
+kv_evict).
 """
 import contextlib
 import ctypes
+import math
 import os
 from collections import namedtuple
 
@@ -22,7 +26,9 @@ __all__ = ["Stats", "Rule", "token_stats", "threshold_transfer", "topk_transfer"
            "transfer_schedule", "block_ranges", "block_causal_mask",
            "workspace_size", "library_path", "load_library", "commit_step", "CommitStep",
            "linear_temperature", "uniform_canvas", "renoise", "StableConfidentStopping",
-           "decaying_threshold"]
+           "decaying_threshold", "Logprobs", "token_logprobs", "token_logprobs_grad", "KVCache",
+           "kv_write", "kv_read", "Attention", "block_attention", "Evicted",
+           "evict_select", "kv_gather", "kv_evict", "KV_PAGE"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libdllm_commit.so")
@@ -33,9 +39,14 @@ SCORE_PROB, SCORE_MARGIN, SCORE_NEG_ENTROPY = 0, 1, 2
 _SCORES = {"prob": SCORE_PROB, "margin": SCORE_MARGIN, "neg_entropy": SCORE_NEG_ENTROPY}
 MAX_L = 4096
 MAX_SUPPRESS = 64
+MAX_TOP = 32
+KV_PAGE = 32
 
 Stats = namedtuple("Stats", ["x0", "prob", "entropy", "margin", "argmax"])
 CommitStep = namedtuple("CommitStep", ["stats", "counts"])
+Logprobs = namedtuple("Logprobs", ["logprob", "entropy", "top_ids", "top_logprobs", "norm"])
+Attention = namedtuple("Attention", ["out", "lse"])
+Evicted = namedtuple("Evicted", ["kept", "lens", "weights"])
 
 
 class _CRule(ctypes.Structure):
@@ -53,6 +64,12 @@ class _CStatsExtra(ctypes.Structure):
 class _CCanvas(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("skip_rows", ctypes.c_int)]
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _lib = None
@@ -87,6 +104,20 @@ _SIGNATURES = {
     "dllm_renoise": (_I32, [_P, _P, _P, _I64, _I64, _P, _P]),
     "dllm_stable_confident_stop": (_I32, [_P, _P, _I64, _I64, _I32, ctypes.c_double, _I32, _P, _P,
                                           _P, _P]),
+    "dllm_token_logprobs": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _I32, _P,
+                                   _I32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dllm_token_logprobs_workspace_size": (ctypes.c_size_t, [_I32, _I64, _I64, _I64, _I32]),
+    "dllm_token_logprobs_grad": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _I32,
+                                        _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "dllm_kv_write": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P]),
+    "dllm_kv_read": (_I32, [_P, _I64, _P, _I64, _I64, _P, _P, _P, _P]),
+    "dllm_block_attention": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64,
+                                    ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dllm_block_attention_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "dllm_attention_weights": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P,
+                                      _I64, ctypes.c_float, _P, _P, _P]),
+    "dllm_evict_select": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P]),
+    "dllm_kv_gather": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _P]),
     "dllm_read_probe": (_I32, [_P, _I64, _I64, _I32, _P, _P]),
     "dllm_stage_timestamps": (_I32, [_P, ctypes.c_size_t, _I32]),
     "dllm_last_error": (ctypes.c_char_p, []),
@@ -619,3 +650,377 @@ class StableConfidentStopping:
                 self.prev.data_ptr(), self.count.data_ptr(), self.done.data_ptr(),
                 _stream(argmax)), "dllm_stable_confident_stop")
         return self.done.bool()
+
+
+# ---------------------------------------------------------------- scores of given tokens
+
+def _same(t, name, dtypes, shape, device):
+    """A contiguous tensor of this shape on the call's device."""
+    _bl(t, name, dtypes, torch.Size(shape))
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _logits_args(logits):
+    _dev(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be (B, L, V)")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be float32 or bfloat16")
+    return DLLM_BF16 if logits.dtype == torch.bfloat16 else DLLM_F32, _row_stride(logits)
+
+
+def _suppress_array(suppress_ids):
+    return (ctypes.c_int32 * max(len(suppress_ids), 1))(*[int(s) for s in suppress_ids])
+
+
+_lp_sizes = {}
+
+
+def _logprobs_workspace(dev, stream, dt, B, L, V, top):
+    key = (dt, B, L, V, top, dev.index)
+    need = _lp_sizes.get(key)
+    if need is None:
+        need = int(load_library().dllm_token_logprobs_workspace_size(dt, B, L, V, top))
+        _lp_sizes[key] = need
+    if need == 0:
+        return None
+    if _capturing(dev):
+        # a buffer of the graph's own, cleared by a node of the graph, so that
+        # graphs captured on one stream and replayed side by side share nothing
+        return torch.zeros(need, dtype=torch.uint8, device=dev)
+    return _workspace(dev, stream, need)
+
+
+def _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace):
+    dt, row_stride = _logits_args(logits)
+    B, L, V = logits.shape
+    dev = logits.device
+    _same(targets, "targets", (torch.int32,), (B, L), dev)
+    top = int(top)
+    if not 0 <= top <= MAX_TOP:
+        raise ValueError(f"top must be in [0, {MAX_TOP}]")
+    sup = _suppress_array(suppress_ids)
+    logprob = torch.empty((B, L), dtype=torch.float32, device=dev)
+    entropy = torch.empty((B, L), dtype=torch.float32, device=dev)
+    norm = torch.empty((B, L, 2), dtype=torch.float32, device=dev)
+    ids = torch.empty((B, L, top), dtype=torch.int32, device=dev) if top else None
+    lps = torch.empty((B, L, top), dtype=torch.float32, device=dev) if top else None
+    with _on(dev):
+        stream = _stream(logits)
+        if workspace is None:
+            workspace = _logprobs_workspace(dev, stream, dt, B, L, V, top)
+        _check(load_library().dllm_token_logprobs(
+            logits.data_ptr(), dt, B, L, V, row_stride, float(temperature), sup,
+            len(suppress_ids), targets.data_ptr(), top, logprob.data_ptr(), entropy.data_ptr(),
+            norm.data_ptr(), ids.data_ptr() if top else None, lps.data_ptr() if top else None,
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0, stream), "dllm_token_logprobs")
+    return Logprobs(logprob, entropy, ids, lps, norm)
+
+
+class _LogprobsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, temperature, suppress_ids, top, workspace):
+        r = _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace)
+        ctx.save_for_backward(logits, targets, r.norm, r.entropy)
+        ctx.temperature, ctx.suppress_ids = temperature, suppress_ids
+        ctx.mark_non_differentiable(*(t for t in r[2:] if t is not None))
+        ctx.set_materialize_grads(False)
+        return tuple(r)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logprob, g_entropy, *_):
+        if g_logprob is None and g_entropy is None:
+            return (None,) * 6
+        logits, targets, norm, entropy = ctx.saved_tensors
+        grad = token_logprobs_grad(
+            logits, targets, norm, entropy,
+            None if g_logprob is None else g_logprob.contiguous(),
+            None if g_entropy is None else g_entropy.contiguous(),
+            temperature=ctx.temperature, suppress_ids=ctx.suppress_ids)
+        return (grad,) + (None,) * 5
+
+
+def token_logprobs(logits, targets, temperature=1.0, suppress_ids=(), top=0, workspace=None):
+    """Scores of given tokens: for (B, L, V) float32 / bfloat16 logits and (B, L)
+    int32 targets, log softmax(logits / temperature) at the target, the
+    position's entropy, and its ``top`` most likely ids with their log
+    probabilities (decreasing, ties by lower id; -1 and -inf where fewer ids
+    have any probability; None when top == 0).  A target outside [0, V), such as
+    -1, marks a position that is not scored: logprob and entropy 0, no gradient.
+
+    Differentiable: logprob and entropy carry the gradient to logits that
+    require one.  ``norm`` (B, L, 2) is what token_logprobs_grad takes.
+    ``workspace``: None, or a zero-filled uint8 tensor that no other call in
+    flight uses.
+    """
+    if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
+        return Logprobs(*_LogprobsFunction.apply(logits, targets, temperature, suppress_ids, top,
+                                                 workspace))
+    return _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace)
+
+
+def token_logprobs_grad(logits, targets, norm, entropy, grad_logprob, grad_entropy=None,
+                        temperature=1.0, suppress_ids=(), out=None):
+    """Gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with
+    respect to the logits, from token_logprobs' norm and entropy.  Either
+    gradient may be None.  ``out`` may be the logits themselves."""
+    dt, row_stride = _logits_args(logits)
+    B, L, V = logits.shape
+    dev = logits.device
+    _same(targets, "targets", (torch.int32,), (B, L), dev)
+    _same(norm, "norm", (torch.float32,), (B, L, 2), dev)
+    _same(entropy, "entropy", (torch.float32,), (B, L), dev)
+    for g, name in ((grad_logprob, "grad_logprob"), (grad_entropy, "grad_entropy")):
+        if g is not None:
+            _same(g, name, (torch.float32,), (B, L), dev)
+    if out is None:
+        out = torch.empty((B, L, V), dtype=logits.dtype, device=dev)
+    _dev(out, "out")
+    if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
+        raise ValueError("out must have the logits' dtype, shape and device")
+    with _on(dev):
+        _check(load_library().dllm_token_logprobs_grad(
+            logits.data_ptr(), dt, B, L, V, row_stride, float(temperature),
+            _suppress_array(suppress_ids), len(suppress_ids), targets.data_ptr(), norm.data_ptr(),
+            entropy.data_ptr(), grad_logprob.data_ptr() if grad_logprob is not None else None,
+            grad_entropy.data_ptr() if grad_entropy is not None else None, out.data_ptr(),
+            _row_stride(out), _stream(logits)), "dllm_token_logprobs_grad")
+    return out
+
+
+# ---------------------------------------------------------------- the 8-bit key/value cache
+
+class KVCache:
+    """A pool of pages of KV_PAGE tokens: keys and values of ``kv_heads`` heads of
+    ``head_dim`` (64, 128 or 256) channels in e4m3, a power-of-two scale per page
+    and head.  Sequences are rows of page numbers (int32 page tables), which the
+    caller hands out.  The byte layout is the library's (include/dllm_commit.h);
+    kv_read gives the values."""
+
+    def __init__(self, num_pages, kv_heads, head_dim, device="cuda"):
+        if head_dim not in (64, 128, 256):
+            raise ValueError("head_dim must be 64, 128 or 256")
+        if num_pages < 1 or kv_heads < 1:
+            raise ValueError("num_pages and kv_heads must be positive")
+        self.num_pages, self.kv_heads, self.head_dim = int(num_pages), int(kv_heads), int(head_dim)
+        shape = (self.num_pages, self.kv_heads, KV_PAGE * self.head_dim)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.k_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
+        self.v_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
+        self.device = self.k.device
+        self._c = _CCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                          self.v_scale.data_ptr(), self.num_pages, self.kv_heads, self.head_dim)
+
+
+def _cache(cache):
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    return _dev(cache.k, "cache"), ctypes.byref(cache._c)
+
+
+def _table(t, name, B, device):
+    """A (B, pages) int32 page table, rows of unit stride (a slice of a larger
+    table will do); returns (pages, row stride)."""
+    _dev(t, name)
+    if t.dtype != torch.int32 or t.dim() != 2 or t.device != device:
+        raise ValueError(f"{name} must be a (B, pages) int32 tensor on {device}")
+    if B is not None and t.shape[0] != B:
+        raise ValueError(f"{name} has {t.shape[0]} rows, not {B}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must have unit stride")
+    return t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _heads(t, name, shape, device):
+    """A (B, L, heads, head_dim) bfloat16 tensor with unit stride along the last
+    dimension; returns its element strides as a C array."""
+    _dev(t, name)
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be a {tuple(shape)} bfloat16 tensor on {device}, not "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.numel() and t.stride(3) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def _ints(t, name, B, device):
+    return None if t is None else _same(t, name, (torch.int32,), (B,), device).data_ptr()
+
+
+def kv_write(cache, k, v, page_table, start, lens=None):
+    """Store k, v (B, L, kv_heads, head_dim) bfloat16 as tokens start[b] ..
+    start[b] + lens[b] - 1 (lens None: L) of every sequence, whose pages
+    page_table (B, pages) names; the sequence then ends there.  Tokens before
+    start[b] stay.  start, lens: (B,) int32."""
+    pool, c = _cache(cache)
+    dev = pool.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be (B, L, kv_heads, head_dim)")
+    B, L = k.shape[:2]
+    ks = _heads(k, "k", (B, L, cache.kv_heads, cache.head_dim), dev)
+    vs = _heads(v, "v", (B, L, cache.kv_heads, cache.head_dim), dev)
+    pages, stride = _table(page_table, "page_table", B, dev)
+    s = _ints(start, "start", B, dev)
+    if s is None:
+        raise ValueError("start must be given")
+    with _on(dev):
+        _check(load_library().dllm_kv_write(c, k.data_ptr(), ks, v.data_ptr(), vs, B, L,
+                                            page_table.data_ptr(), pages, stride, s,
+                                            _ints(lens, "lens", B, dev), _stream(pool)),
+               "dllm_kv_write")
+
+
+def kv_read(cache, page_table, lens):
+    """(k, v), each (B, KV_PAGE * pages, kv_heads, head_dim) bfloat16: the values
+    the cache stands for, 0 past lens[b]."""
+    pool, c = _cache(cache)
+    dev = pool.device
+    pages, stride = _table(page_table, "page_table", None, dev)
+    B = page_table.shape[0]
+    n = _ints(lens, "lens", B, dev)
+    k = torch.empty((B, pages * KV_PAGE, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16,
+                    device=dev)
+    v = torch.empty_like(k)
+    with _on(dev):
+        _check(load_library().dllm_kv_read(c, B, page_table.data_ptr(), pages, stride, n,
+                                           k.data_ptr(), v.data_ptr(), _stream(pool)),
+               "dllm_kv_read")
+    return k, v
+
+
+_attn_sizes = {}
+
+
+def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, block_len=0,
+                    scale=None, weights=None, out=None, lse=None, workspace=None):
+    """Attention of q (B, L, q_heads, head_dim) bfloat16 over the cached tokens
+    t < kv_lens[b]; with block_len > 0 only t // block_len <= pos // block_len
+    for the query at pos = q_start[b] + l (the mask of block_causal_mask;
+    block_len = 1 is causal).  Query head h reads key/value head
+    h // (q_heads // kv_heads).  scale: 1 / sqrt(head_dim) by default.
+
+    Returns Attention(out, lse): out like q, lse (B, q_heads, L) float32 (natural
+    log).  A query that attends to nothing gives 0 and -inf; queries
+    l >= q_lens[b] are not written (0 and -inf in outputs allocated here).
+    ``weights`` (B, KV_PAGE * pages) float32: every cached token's attention
+    weight, summed over queries and heads, is added to it (see kv_evict).
+    ``workspace``: None, or a uint8 tensor that no other call in flight uses.
+    """
+    pool, c = _cache(cache)
+    dev = pool.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be (B, L, q_heads, head_dim)")
+    B, L, Hq, D = q.shape
+    qs = _heads(q, "q", (B, L, Hq, cache.head_dim), dev)
+    pages, stride = _table(page_table, "page_table", B, dev)
+    n = _ints(kv_lens, "kv_lens", B, dev)
+    if n is None:
+        raise ValueError("kv_lens must be given")
+    qstart, qlens = _ints(q_start, "q_start", B, dev), _ints(q_lens, "q_lens", B, dev)
+    if out is None:
+        out = (torch.empty if q_lens is None else torch.zeros)((B, L, Hq, D), dtype=torch.bfloat16,
+                                                                device=dev)
+    os_ = _heads(out, "out", (B, L, Hq, D), dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
+        if q_lens is not None:
+            lse.fill_(-math.inf)
+    _same(lse, "lse", (torch.float32,), (B, Hq, L), dev)
+    if weights is not None:
+        _same(weights, "weights", (torch.float32,), (B, pages * KV_PAGE), dev)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    lib = load_library()
+    with _on(dev):
+        if workspace is None:
+            key = (B, L, Hq, cache.kv_heads, D, pages, dev.index)
+            need = _attn_sizes.get(key)
+            if need is None:
+                need = int(lib.dllm_block_attention_workspace_size(B, L, Hq, cache.kv_heads, D,
+                                                                   pages))
+                _attn_sizes[key] = need
+            # any content will do: a block of torch's allocator per call, so that
+            # neither streams nor captured graphs share one
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        stream = _stream(pool)
+        head = (c, q.data_ptr(), qs, B, L, Hq, page_table.data_ptr(), pages, stride, n, qstart,
+                qlens, int(block_len), scale)
+        _check(lib.dllm_block_attention(
+            *head, out.data_ptr(), os_, lse.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0, stream), "dllm_block_attention")
+        if weights is not None:
+            _check(lib.dllm_attention_weights(*head, lse.data_ptr(), weights.data_ptr(), stream),
+                   "dllm_attention_weights")
+    return Attention(out, lse)
+
+
+def evict_select(weights, kv_lens, budget, sink=0, recent=0, new_T=None):
+    """The tokens that stay when each cache is cut to ``budget`` tokens: all of
+    them if there are no more; else the first ``sink``, the last ``recent``, and
+    the ones of largest weight (ties: the lower position).  weights (B, T)
+    float32, kv_lens (B,) int32.  Returns Evicted(kept (B, budget) int32
+    increasing, -1 behind the last; lens (B,) int32; their weights (B, new_T),
+    0 behind the last)."""
+    _dev(weights, "weights")
+    if weights.dtype != torch.float32 or weights.dim() != 2 or \
+            (weights.shape[1] > 1 and weights.stride(1) != 1):
+        raise ValueError("weights must be a (B, T) float32 tensor with rows of unit stride")
+    B, T = weights.shape
+    dev = weights.device
+    n = _ints(kv_lens, "kv_lens", B, dev)
+    budget = int(budget)
+    if budget < 1:
+        raise ValueError("budget must be positive")
+    new_T = budget if new_T is None else int(new_T)
+    kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
+    lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    new_w = torch.empty((B, new_T), dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check(load_library().dllm_evict_select(
+            weights.data_ptr(), B, T, weights.stride(0) if B > 1 else T, n, budget, int(sink),
+            int(recent), kept.data_ptr(), lens.data_ptr(), new_w.data_ptr(), new_T,
+            _stream(weights)), "dllm_evict_select")
+    return Evicted(kept, lens, new_w)
+
+
+def kv_gather(cache, page_table, kept, counts, new_pages):
+    """Token j < counts[b] on the pages of new_pages (B, pages) becomes token
+    kept[b, j] of the sequence on page_table.  kept increases along its rows; no
+    page of new_pages may be in use."""
+    pool, c = _cache(cache)
+    dev = pool.device
+    pages, stride = _table(page_table, "page_table", None, dev)
+    B = page_table.shape[0]
+    npages, nstride = _table(new_pages, "new_pages", B, dev)
+    if not isinstance(kept, torch.Tensor) or kept.dim() != 2:
+        raise ValueError("kept must be (B, n)")
+    _same(kept, "kept", (torch.int32,), (B, kept.shape[1]), dev)
+    counts_p = _ints(counts, "counts", B, dev)
+    with _on(dev):
+        _check(load_library().dllm_kv_gather(
+            c, B, page_table.data_ptr(), pages, stride, kept.data_ptr(), kept.shape[1], counts_p,
+            new_pages.data_ptr(), npages, nstride, _stream(pool)), "dllm_kv_gather")
+
+
+def kv_evict(cache, page_table, kv_lens, weights, budget, new_pages, sink=0, recent=0):
+    """Cut every sequence's cache to ``budget`` tokens by accumulated attention
+    weight (evict_select) and move the kept tokens to new_pages (B, at least
+    ceil(budget / KV_PAGE)), free pages of the same pool (kv_gather); the old
+    pages are then free.  Returns Evicted: the kept positions, the new lengths,
+    and the kept tokens' weights (B, KV_PAGE * new_pages.shape[1]), which go on
+    accumulating."""
+    pool, _ = _cache(cache)
+    pages, _ = _table(page_table, "page_table", None, pool.device)
+    npages, _ = _table(new_pages, "new_pages", page_table.shape[0], pool.device)
+    if npages * KV_PAGE < int(budget):
+        raise ValueError("new_pages cannot hold budget tokens")
+    _same(weights, "weights", (torch.float32,), (page_table.shape[0], pages * KV_PAGE),
+          pool.device)
+    r = evict_select(weights, kv_lens, budget, sink, recent, new_T=npages * KV_PAGE)
+    kv_gather(cache, page_table, r.kept, r.lens, new_pages)
+    return r

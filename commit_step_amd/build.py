@@ -12,7 +12,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/token_stats.hip", "csrc/token_stats_full.hip", "csrc/transfer.hip",
-           "csrc/uniform.hip", "csrc/read_probe.hip"]
+           "csrc/uniform.hip", "csrc/read_probe.hip", "csrc/logprobs.hip", "csrc/kv_cache.hip",
+           "csrc/attention.hip", "csrc/evict.hip"]
 LIB = os.path.join(HERE, "libdllm_commit.so")
 STAGES_LIB = os.path.join(HERE, "libdllm_commit_stages.so")
 

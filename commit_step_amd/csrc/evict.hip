@@ -1,0 +1,157 @@
+// dllm_evict_select: the tokens of each cache that an eviction keeps.
+//
+// One workgroup per sequence.  The weights' order-preserving keys (best first,
+// common.h; a protected token's key is 0, before every weight's) are selected
+// by radix: three histograms of 11, 11 and 10 bits find the budget-th smallest
+// key, then two sweeps place the kept positions in order, each wave its own
+// run of the sequence, with one prefix over the waves between them.  The
+// weights are read from HBM once and from L2 afterwards; the work is bound by
+// the sweeps' latency in one workgroup.
+#include <algorithm>
+
+#include "common.h"
+
+namespace dllm {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWaves = kSelThreads / 64;
+
+struct SelectArgs {
+  const float *weights;
+  int64_t weights_stride, T, budget, sink, recent, new_T;
+  const int32_t *lens;
+  int32_t *kept, *new_lens;
+  float *new_weights;
+};
+
+__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a) {
+  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t s_digit, s_below;
+  __shared__ int s_wave[kSelThreads / 64], s_less[kSelWaves], s_same[kSelWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t b = blockIdx.x;
+  const float *w = a.weights + b * a.weights_stride;
+  const int n = (int)(a.lens[b] < 0 ? 0 : min((int64_t)a.lens[b], a.T));
+  const int keep = (int)min((int64_t)n, a.budget);
+  int32_t *kept = a.kept + b * a.budget;
+  float *nw = a.new_weights ? a.new_weights + b * a.new_T : nullptr;
+  if (tid == 0) a.new_lens[b] = keep;
+  for (int64_t j = keep + tid; j < a.budget; j += kSelThreads) kept[j] = -1;
+  if (nw)
+    for (int64_t j = keep + tid; j < a.new_T; j += kSelThreads) nw[j] = 0.f;
+  if (n <= a.budget) {
+    for (int j = tid; j < keep; j += kSelThreads) {
+      kept[j] = j;
+      if (nw) nw[j] = w[j];
+    }
+    return;
+  }
+  const int sink = (int)a.sink, tail = n - (int)a.recent;
+  auto key_of = [&](int t) -> uint32_t {
+    return t < sink || t >= tail ? 0u : conf_key(w[t]);
+  };
+
+  // the keep-th smallest key: digit by digit from the top
+  uint32_t prefix = 0, mask = 0;
+  uint32_t want = (uint32_t)keep;             // still to find among keys matching prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
+    for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int t = tid; t < n; t += kSelThreads) {
+      const uint32_t k = key_of(t);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1u);
+    }
+    __syncthreads();
+    // inclusive prefix over the bins, two per thread; the digit's bin is the
+    // first whose prefix reaches want
+    const uint32_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
+    int sum = (int)(h0 + h1);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (lane == 63) s_wave[wave] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < wave; ++i) before += s_wave[i];
+    const uint32_t incl = (uint32_t)(before + sum), excl = incl - h0 - h1;
+    if (excl < want && want <= incl) {
+      const bool first = want <= excl + h0;
+      s_digit = (uint32_t)(2 * tid + (first ? 0 : 1));
+      s_below = first ? excl : excl + h0;
+    }
+    __syncthreads();
+    prefix |= s_digit << shift;
+    mask |= bits << shift;
+    want -= s_below;
+    __syncthreads();
+  }
+
+  // keys below the threshold all stay, and the first `want` equal to it
+  const int run = ((n + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
+  const int lo = min(wave * run, n), hi = min(lo + run, n);
+  int less = 0, same = 0;
+  for (int t0 = lo; t0 < hi; t0 += 64) {
+    const int t = t0 + lane;
+    const uint32_t k = t < hi ? key_of(t) : ~0u;
+    less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t < hi && k < prefix));
+    same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t < hi && k == prefix));
+  }
+  if (lane == 0) { s_less[wave] = less; s_same[wave] = same; }
+  __syncthreads();
+  int at_less = 0, at_same = 0;
+  for (int i = 0; i < wave; ++i) { at_less += s_less[i]; at_same += s_same[i]; }
+  const uint64_t below = (1ull << lane) - 1ull;
+  for (int t0 = lo; t0 < hi; t0 += 64) {
+    const int t = t0 + lane;
+    const uint32_t k = t < hi ? key_of(t) : ~0u;
+    const bool is_less = t < hi && k < prefix, is_same = t < hi && k == prefix;
+    const uint64_t ml = __builtin_amdgcn_ballot_w64(is_less);
+    const uint64_t ms = __builtin_amdgcn_ballot_w64(is_same);
+    const int rl = at_less + __builtin_popcountll(ml & below);
+    const int rs = at_same + __builtin_popcountll(ms & below);
+    if (is_less || (is_same && rs < (int)want)) {
+      const int j = rl + min(rs, (int)want);
+      kept[j] = t;
+      if (nw) nw[j] = w[t];
+    }
+    at_less += __builtin_popcountll(ml);
+    at_same += __builtin_popcountll(ms);
+  }
+}
+
+}  // namespace
+}  // namespace dllm
+
+using namespace dllm;
+
+extern "C" int dllm_evict_select(const float *weights, int64_t B, int64_t T,
+                                 int64_t weights_stride, const int32_t *kv_lens, int64_t budget,
+                                 int64_t sink, int64_t recent, int32_t *kept, int32_t *new_lens,
+                                 float *new_weights, int64_t new_T, hipStream_t stream) {
+  const char *who = "dllm_evict_select";
+  if (B < 0 || T < 0 || T > 0x7fffffffLL - kSelThreads * 64)
+    return fail(DLLM_ERR_ARG, "%s: B must be >= 0 and T in [0, 2^31 - 2^16)", who);
+  if (budget < 1 || budget > 0x7fffffffLL)
+    return fail(DLLM_ERR_ARG, "%s: budget must be in [1, 2^31)", who);
+  if (sink < 0 || recent < 0 || sink > budget || recent > budget - sink)
+    return fail(DLLM_ERR_ARG, "%s: sink and recent must be >= 0 and at most budget together", who);
+  if (weights_stride < T) return fail(DLLM_ERR_ARG, "%s: weights_stride < T", who);
+  if (new_weights && new_T < budget) return fail(DLLM_ERR_ARG, "%s: new_T < budget", who);
+  if (B > 0xffffffffLL / kSelThreads)
+    return fail(DLLM_ERR_UNSUPPORTED, "%s: too many sequences in one call", who);
+  if (B == 0) return ok();
+  if (!weights || !kv_lens || !kept || !new_lens)
+    return fail(DLLM_ERR_ARG, "%s: weights, kv_lens, kept and new_lens must be non-NULL", who);
+  if ((const void *)new_weights == (const void *)weights)
+    return fail(DLLM_ERR_ARG, "%s: new_weights aliases weights", who);
+  const SelectArgs a{weights, weights_stride, T, budget, sink, recent, new_T,
+                     kv_lens, kept, new_lens, new_weights};
+  hipLaunchKernelGGL(evict_select_kernel, dim3((uint32_t)B), dim3(kSelThreads), 0, stream, a);
+  return check_launch(who);
+}

@@ -399,6 +399,227 @@ int dllm_stable_confident_stop(const int32_t *argmax, const float *entropy,
                                int32_t *prev_argmax, int32_t *stable_steps,
                                uint8_t *done, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Scores of given tokens: log probabilities, entropy, top alternatives, and
+ * the gradient.  dllm_token_stats scores its own proposal; this scores tokens
+ * the caller names: the tokens a finished canvas holds (evaluation, reranking,
+ * served log probabilities), or the clean tokens of a masked-diffusion
+ * training step.
+ * -------------------------------------------------------------------------*/
+
+/* top alternatives per position dllm_token_logprobs can list */
+#define DLLM_MAX_TOP 32
+
+/* dllm_token_logprobs: with p = softmax(logits / temperature) over the
+ * unsuppressed ids of each position and t = targets[b, l]:
+ *   logprob[b, l] = log p_t (natural log; -inf for a suppressed target),
+ *   entropy[b, l] = -sum p log p,
+ *   top_ids / top_logprobs[b, l, 0 .. top-1] = the ids of largest logit in
+ *       decreasing order, equal logits by lower id, and log p of each; ids of
+ *       zero probability are not listed: entries past the last one are
+ *       (-1, -inf),
+ *   norm[b, l] = (M, log sum exp((logits - M) / temperature)), M the largest
+ *       logit: what dllm_token_logprobs_grad needs of the forward pass.
+ *
+ *   logits, dtype, row_stride, suppress_ids  as in dllm_token_stats.
+ *   temperature  finite, > 0.
+ *   targets      (B, L) int32 DEVICE.  A target outside [0, V) marks a
+ *                position that is not scored: its logits are not read, its
+ *                logprob and entropy are 0, its alternatives (-1, -inf), its
+ *                norm (0, 0), and its gradient 0.
+ *   top          0 .. DLLM_MAX_TOP; top_ids and top_logprobs may be NULL when 0.
+ *   logprob, entropy (B, L), norm (B, L, 2) or NULL, top_ids (B, L, top) int32,
+ *                top_logprobs (B, L, top): DEVICE outputs, float32.
+ *   workspace    as in dllm_token_stats, of at least
+ *                dllm_token_logprobs_workspace_size() bytes: zero-filled before
+ *                its first use, left zero-filled by every call.
+ * NaN safety as in dllm_token_stats (a NaN logit counts as -inf; a position
+ * whose unsuppressed logits are all -inf is uniform over the unsuppressed ids,
+ * one with +inf logits over its +inf ids); no output is NaN. */
+int dllm_token_logprobs(const void *logits, int dtype, int64_t B, int64_t L, int64_t V,
+                        int64_t row_stride, float temperature, const int32_t *suppress_ids,
+                        int n_suppress, const int32_t *targets, int top, float *logprob,
+                        float *entropy, float *norm, int32_t *top_ids, float *top_logprobs,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dllm_token_logprobs needs for this shape on the current
+ * device.  Returns 0 on bad arguments. */
+size_t dllm_token_logprobs_workspace_size(int dtype, int64_t B, int64_t L, int64_t V, int top);
+
+/* dllm_token_logprobs_grad: the gradient of sum(grad_logprob * logprob +
+ * grad_entropy * entropy) with respect to the logits,
+ *   grad[b, l, v] = (g (v == t) - p_v (g + h (log p_v + entropy))) / temperature
+ * with g = grad_logprob[b, l], h = grad_entropy[b, l]; 0 at suppressed ids and
+ * at every id of a position that is not scored (whose g, h, norm and logits
+ * are not read).  p_v is recomputed from the logits and the forward pass's
+ * norm and entropy.
+ *   grad_logprob, grad_entropy  (B, L) float32 DEVICE, either may be NULL (0).
+ *   grad         (B, L, V) DEVICE output of the logits' dtype, position (b, l)
+ *                at element (b*L + l) * grad_stride, grad_stride >= V.  It may
+ *                be the logits themselves (same pointer and stride): every
+ *                element is read before it is written.  Any other overlap is
+ *                an error of the caller.
+ * The other arguments are those of the forward call. */
+int dllm_token_logprobs_grad(const void *logits, int dtype, int64_t B, int64_t L, int64_t V,
+                             int64_t row_stride, float temperature, const int32_t *suppress_ids,
+                             int n_suppress, const int32_t *targets, const float *norm,
+                             const float *entropy, const float *grad_logprob,
+                             const float *grad_entropy, void *grad, int64_t grad_stride,
+                             hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The key/value cache of block decoding, in 8 bits.
+ *
+ * Block decoding runs the model over one block at a time against the cached
+ * keys and values of the finished prefix (mlx-arsenal "dLLM block decoding":
+ * the block loop keeps its cache outside the commit step).  The cache is a
+ * pool of pages of DLLM_KV_PAGE tokens; a sequence is a row of page numbers.
+ * Keys and values are stored as e4m3 codes (OCP 8-bit float: 4 exponent bits,
+ * bias 7, 3 mantissa bits, largest value 448) with one power-of-two scale per
+ * page and head, for keys and values apart: value = code * scale.  A power of
+ * two costs a floating-point code no precision, is applied exactly, and lets a
+ * page be coded again in a larger scale without error in any normal code.
+ *   scale     the smallest power of two s in [2^-100, 2^119] with max |x| <=
+ *             448 s over the page's finite elements of that head (2^119 if
+ *             none is); codes are x / s rounded to nearest, ties to even.  NaN
+ *             is stored as 0, and anything beyond +-448 s, +-inf too, as
+ *             +-448 s: every stored value is finite.
+ *   layout    of one page and head, 32 x D bytes each:
+ *             k: byte ((d / 16) * 32 + t) * 16 + d % 16 holds element d of
+ *                token t;
+ *             v: byte (d / 32) * 1024 + ((t / 4) % 2) * 512 + (d % 32) * 16 +
+ *                (t / 8) * 4 + t % 4;
+ *             so that the 64 lanes of a wave load a page in consecutive
+ *             16-byte pieces, each lane the elements its matrix operand needs.
+ * -------------------------------------------------------------------------*/
+#define DLLM_KV_PAGE 32
+
+/* k, v: (num_pages, kv_heads, 32 * head_dim) bytes, 16-byte aligned; k_scale,
+ * v_scale: (num_pages, kv_heads) float32; all DEVICE, caller-owned.
+ * head_dim is 64, 128 or 256. */
+typedef struct {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t num_pages;
+  int32_t kv_heads;
+  int32_t head_dim;
+} dllm_kv_cache;
+
+/* Page tables, shared by the calls below: page_table[b * table_stride + j] is
+ * the page of tokens 32 j .. 32 j + 31 of sequence b, j < max_pages; int32
+ * DEVICE.  A page number outside [0, num_pages) stands for no page: nothing is
+ * written to it, and its tokens are neither read nor attended to.  Lengths and
+ * positions are int32 DEVICE arrays of B entries; a length beyond
+ * 32 * max_pages counts as 32 * max_pages, a negative one as 0. */
+
+/* dllm_kv_write: stores the keys and values of tokens start[b] ..
+ * start[b] + lens[b] - 1 of every sequence; afterwards the sequence is meant
+ * to end there.  Tokens of its first page before start[b] stay: the page's
+ * scale is then the larger of its old one and the one the new tokens need, and
+ * the old tokens are coded again if it grew.  Slots behind the last token are
+ * left as they were.  Writing a block again each step (start[b] unchanged)
+ * therefore replaces it.  With start[b] a multiple of 32 no older token
+ * is touched.
+ *   k, v     (B, L, kv_heads, head_dim) bfloat16, element strides k_strides[3],
+ *            v_strides[3] (HOST) of the first three dimensions, unit stride
+ *            along the last.
+ *   lens     tokens of each sequence to store, at most L (more counts as L), or
+ *            NULL for L.  A negative start writes nothing.  Tokens past the
+ *            end of the page table are dropped.
+ * No page may appear twice among the pages written by one call. */
+int dllm_kv_write(const dllm_kv_cache *cache, const void *k, const int64_t *k_strides,
+                  const void *v, const int64_t *v_strides, int64_t B, int64_t L,
+                  const int32_t *page_table, int64_t max_pages, int64_t table_stride,
+                  const int32_t *start, const int32_t *lens, hipStream_t stream);
+
+/* dllm_kv_read: the values the cache stands for, exact in bfloat16: k_out,
+ * v_out (B, 32 * max_pages, kv_heads, head_dim) bfloat16 contiguous, 0 at
+ * tokens past lens[b] and on missing pages. */
+int dllm_kv_read(const dllm_kv_cache *cache, int64_t B, const int32_t *page_table,
+                 int64_t max_pages, int64_t table_stride, const int32_t *lens, void *k_out,
+                 void *v_out, hipStream_t stream);
+
+/* dllm_block_attention: attention of B x L queries over the cached tokens,
+ *   s_t = scale q . k_t,  p = softmax(s),  out = sum p_t v_t,
+ *   lse = log sum exp(s_t),
+ * over the tokens t < kv_lens[b] of the query's sequence and, with
+ * block_len > 0, t / block_len <= pos / block_len, pos = q_start[b] + l: the
+ * mask of dllm_block_causal_mask (block_len = 1: causal), which is never
+ * materialised.  block_len = 0: every cached token, as a block of decoding
+ * sees its prefix and itself (the block's own keys written first).  A query
+ * that attends to nothing gives out = 0, lse = -inf.
+ *   q        (B, L, q_heads, head_dim) bfloat16, element strides q_strides[3]
+ *            (HOST) of the first three dimensions, unit stride along the
+ *            last; q_heads a multiple of kv_heads, query head h reading
+ *            key/value head h / (q_heads / kv_heads).
+ *   q_start  positions of the first queries, or NULL (0); used by block_len
+ *            only; a negative one counts as 0.
+ *   q_lens   queries of each sequence, or NULL (L): outputs of queries
+ *            l >= q_lens[b] are left as they were.
+ *   scale    finite, > 0.
+ *   out      as q, bfloat16, element strides out_strides[3]; must not overlap q.
+ *   lse      (B, q_heads, L) float32, natural log.
+ *   workspace at least dllm_block_attention_workspace_size() bytes, 16-byte
+ *            aligned, of any content; two calls in flight at once must not
+ *            share one.
+ * Products of a query and a key are exact and summed in float32; a weight is
+ * rounded to 11 bits before it multiplies the value, and the sums of weights
+ * and values are float32. */
+int dllm_block_attention(const dllm_kv_cache *cache, const void *q, const int64_t *q_strides,
+                         int64_t B, int64_t L, int64_t q_heads, const int32_t *page_table,
+                         int64_t max_pages, int64_t table_stride, const int32_t *kv_lens,
+                         const int32_t *q_start, const int32_t *q_lens, int64_t block_len,
+                         float scale, void *out, const int64_t *out_strides, float *lse,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dllm_block_attention needs on the current device (a pure
+ * function of the arguments and the device).  Returns 0 on bad arguments. */
+size_t dllm_block_attention_workspace_size(int64_t B, int64_t L, int64_t q_heads,
+                                           int64_t kv_heads, int64_t head_dim,
+                                           int64_t max_pages);
+
+/* dllm_attention_weights: adds to weights[b, t] the attention weight that
+ * cached token t received, sum over the queries and query heads of
+ * exp(s_t - lse), for the same arguments and the lse of dllm_block_attention.
+ * weights (B, 32 * max_pages) float32, read and written at t < kv_lens[b]
+ * only; each entry is summed by one workgroup in a fixed order. */
+int dllm_attention_weights(const dllm_kv_cache *cache, const void *q, const int64_t *q_strides,
+                           int64_t B, int64_t L, int64_t q_heads, const int32_t *page_table,
+                           int64_t max_pages, int64_t table_stride, const int32_t *kv_lens,
+                           const int32_t *q_start, const int32_t *q_lens, int64_t block_len,
+                           float scale, const float *lse, float *weights, hipStream_t stream);
+
+/* dllm_evict_select: which tokens of each cache to keep when it is cut down to
+ * `budget`: with n = kv_lens[b], every token when n <= budget; else the first
+ * `sink`, the last `recent`, and the tokens of largest weight among the
+ * others, budget in all (the ranking rules' order: a NaN weight counts as
+ * -inf, -0 equals +0, equal weights keep the lower position).
+ *   weights  (B, T) float32 at row stride weights_stride.
+ *   kept     (B, budget) int32: the kept positions in increasing order, -1
+ *            behind the last.
+ *   new_lens (B) int32: min(n, budget).
+ *   new_weights (B, new_T) float32 or NULL: the kept tokens' weights, 0 behind
+ *            the last; new_T >= budget.
+ * n is kv_lens[b] cut to [0, T].  budget >= 1, sink, recent >= 0,
+ * sink + recent <= budget, T < 2^31. */
+int dllm_evict_select(const float *weights, int64_t B, int64_t T, int64_t weights_stride,
+                      const int32_t *kv_lens, int64_t budget, int64_t sink, int64_t recent,
+                      int32_t *kept, int32_t *new_lens, float *new_weights, int64_t new_T,
+                      hipStream_t stream);
+
+/* dllm_kv_gather: token j < counts[b] of the sequence on the pages of
+ * new_table becomes token kept[b * kept_stride + j] of the sequence on the
+ * pages of page_table.  A moved page's scale is chosen from the values it then
+ * holds, as dllm_kv_write does.  kept must increase along each row (as
+ * dllm_evict_select gives it); an entry outside [0, 32 * max_pages) or on a
+ * missing page gives a zero token.  The slots behind the last token of the
+ * last new page are zeroed.  No page of new_table may appear twice, or in
+ * page_table. */
+int dllm_kv_gather(const dllm_kv_cache *cache, int64_t B, const int32_t *page_table,
+                   int64_t max_pages, int64_t table_stride, const int32_t *kept,
+                   int64_t kept_stride, const int32_t *counts, const int32_t *new_table,
+                   int64_t new_pages, int64_t new_stride, hipStream_t stream);
+
 /* Measurement helper, not a step of the commit: the stage timestamps of the
  * last dllm_token_stats / dllm_commit_step launch (of either launch shape)
  * in a library built with stage timestamps (libdllm_commit_stages.so, built by

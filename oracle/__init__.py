@@ -32,6 +32,7 @@ from .rules import (threshold_transfer, topk_transfer, factor_transfer,
 from .step import commit_step, apply_step, counts, rank_rule, StepResult
 from .uniform import (linear_temperature, uniform_canvas, renoise, StableConfidentStopping,
                       decode_uniform)
+from . import kv, scores
 
 __all__ = [
     "philox4x32_10", "philox_words", "uniform_from_word", "gumbel_noise",
@@ -41,5 +42,5 @@ __all__ = [
     "block_ranges", "block_causal_mask", "decaying_threshold",
     "commit_step", "apply_step", "counts", "rank_rule", "StepResult",
     "linear_temperature", "uniform_canvas", "renoise", "StableConfidentStopping",
-    "decode_uniform",
+    "decode_uniform", "kv", "scores",
 ]
