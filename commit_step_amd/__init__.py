@@ -115,7 +115,8 @@ _SIGNATURES = {
                                     ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "dllm_block_attention_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _I64]),
     "dllm_attention_weights": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P,
-                                      _I64, ctypes.c_float, _P, _P, _P]),
+                                      _I64, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dllm_attention_weights_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
     "dllm_evict_select": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P]),
     "dllm_kv_gather": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _P]),
     "dllm_read_probe": (_I32, [_P, _I64, _I64, _I32, _P, _P]),
@@ -896,8 +897,20 @@ def kv_read(cache, page_table, lens):
 _attn_sizes = {}
 
 
+def _attn_size(B, L, Hq, H, D, pages, device):
+    """Workspace bytes of (block_attention, its weights)."""
+    key = (B, L, Hq, H, D, pages, device.index)
+    need = _attn_sizes.get(key)
+    if need is None:
+        lib = load_library()
+        need = (int(lib.dllm_block_attention_workspace_size(B, L, Hq, H, D, pages)),
+                int(lib.dllm_attention_weights_workspace_size(B, L, Hq, H, pages)))
+        _attn_sizes[key] = need
+    return need
+
+
 def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, block_len=0,
-                    scale=None, weights=None, out=None, lse=None, workspace=None):
+                    scale=None, weights=None, out=None, lse=None):
     """Attention of q (B, L, q_heads, head_dim) bfloat16 over the cached tokens
     t < kv_lens[b]; with block_len > 0 only t // block_len <= pos // block_len
     for the query at pos = q_start[b] + l (the mask of block_causal_mask;
@@ -909,7 +922,6 @@ def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, bl
     l >= q_lens[b] are not written (0 and -inf in outputs allocated here).
     ``weights`` (B, KV_PAGE * pages) float32: every cached token's attention
     weight, summed over queries and heads, is added to it (see kv_evict).
-    ``workspace``: None, or a uint8 tensor that no other call in flight uses.
     """
     pool, c = _cache(cache)
     dev = pool.device
@@ -936,26 +948,21 @@ def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, bl
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     lib = load_library()
     with _on(dev):
-        if workspace is None:
-            key = (B, L, Hq, cache.kv_heads, D, pages, dev.index)
-            need = _attn_sizes.get(key)
-            if need is None:
-                need = int(lib.dllm_block_attention_workspace_size(B, L, Hq, cache.kv_heads, D,
-                                                                   pages))
-                _attn_sizes[key] = need
-            # any content will do: a block of torch's allocator per call, so that
-            # neither streams nor captured graphs share one
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        need, need_w = _attn_size(B, L, Hq, cache.kv_heads, D, pages, dev)
+        if weights is not None:
+            need = max(need, need_w)
+        # any content will do: a block of torch's allocator per call, so that
+        # neither streams nor captured graphs share one
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        ws_p = ws.data_ptr() if need else None
         stream = _stream(pool)
         head = (c, q.data_ptr(), qs, B, L, Hq, page_table.data_ptr(), pages, stride, n, qstart,
                 qlens, int(block_len), scale)
-        _check(lib.dllm_block_attention(
-            *head, out.data_ptr(), os_, lse.data_ptr(),
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() if workspace is not None else 0, stream), "dllm_block_attention")
+        _check(lib.dllm_block_attention(*head, out.data_ptr(), os_, lse.data_ptr(), ws_p, need,
+                                        stream), "dllm_block_attention")
         if weights is not None:
-            _check(lib.dllm_attention_weights(*head, lse.data_ptr(), weights.data_ptr(), stream),
-                   "dllm_attention_weights")
+            _check(lib.dllm_attention_weights(*head, lse.data_ptr(), weights.data_ptr(), ws_p, need,
+                                              stream), "dllm_attention_weights")
     return Attention(out, lse)
 
 

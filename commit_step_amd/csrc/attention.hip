@@ -14,13 +14,15 @@
 // cache keeps a page's values in that token order (kv_dev.h): no weight
 // crosses lanes and no tile goes through LDS.
 //
-// p is biased by 2^14, so float16 keeps 11 bits of it down to 2^-28 and
-// counts weights down to 2^-39; pages whose value scale is smaller than the largest seen
-// (exponent E) have their p scaled by the difference, so the accumulator is in
-// units of 2^E.
+// p is biased by 2^14, so float16 keeps 11 bits of it down to 2^-28 and counts
+// weights down to 2^-39.  Pages whose value scale is smaller than the largest
+// seen (exponent E) have their p scaled by the difference, so the accumulator
+// is in units of 2^E.
 //
-// The cache is split along its tokens over workgroups when there are few
-// columns; a second kernel joins the parts.
+// A workgroup is CW column waves times KW token waves: the column waves read
+// the same pages (from the CU's cache), the token waves take turns at the pages
+// and join through LDS.  When that leaves CUs idle the cache is also split
+// along its tokens over workgroups, and a second kernel joins the parts.
 #include <string.h>
 
 #include <algorithm>
@@ -36,9 +38,13 @@ int check_table(const char *who, const char *name, const int32_t *table, int64_t
 namespace {
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr int kAttnThreads = 256;
-constexpr int kAttnWaves = kAttnThreads / 64;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWaves = kJoinThreads / 64;
 constexpr float kBias = 14.0f;          // weights are held as 2^14 p
+// The maximum that weights are taken against follows the true one when it has
+// risen by more than this (base 2): weights stay below 2^15, within float16,
+// and the accumulators are rescaled rarely.
+constexpr float kRise = 1.0f;
 
 struct AttnArgs {
   const uint16_t *q;
@@ -50,7 +56,7 @@ struct AttnArgs {
   int64_t num_pages;
   int64_t max_pages, table_stride;
   const int32_t *table, *kv_lens, *q_start, *q_lens;
-  int64_t block_len;
+  uint32_t block_len;       // 0: no mask
   int64_t B;
   int H, G, L;
   int ncols;                // L * G
@@ -62,7 +68,11 @@ struct AttnArgs {
   float *lse;
   float *part_o;            // [B * H * ncols][splits][D]
   float *part_ml;           // [B * H * ncols][splits][2]
-  float *weights;           // dllm_attention_weights
+  // dllm_attention_weights
+  float *weights;
+  float *part_w;            // [parts][B][T]
+  int parts, shares;        // H * shares
+  int token_groups;
 };
 
 // The columns of one wave tile: lane i of each half is column c0 + i.
@@ -81,8 +91,9 @@ __device__ __forceinline__ Column column(const AttnArgs &a, int64_t b, int64_t c
   r.on = c < a.ncols && r.l < q_len;
   r.lim = r.on ? n : 0;
   if (a.block_len > 0 && r.on) {
-    const int64_t s = a.q_start ? max((int64_t)a.q_start[b], (int64_t)0) : 0;
-    r.lim = (int)min((int64_t)n, ((s + r.l) / a.block_len + 1) * a.block_len);
+    // positions and block lengths are below 2^32 and 2^31: a 32-bit division
+    const uint32_t pos = (a.q_start ? (uint32_t)max(a.q_start[b], 0) : 0u) + (uint32_t)r.l;
+    r.lim = (int)min((uint64_t)n, (uint64_t)(pos / a.block_len + 1u) * a.block_len);
   }
   return r;
 }
@@ -154,20 +165,18 @@ struct Tile {
 };
 
 // S^T of one page: tokens x columns, in the keys' own unit.
-template <int D, int QT>
-__device__ __forceinline__ void score_page(const u32x4 (&kw)[D / 32], float ks,
-                                           const bf16x8 (&q)[QT][D / 16], f32x16 (&s)[QT]) {
+template <int D>
+__device__ __forceinline__ f32x16 score_page(const u32x4 (&kw)[D / 32], float ks,
+                                             const bf16x8 (&q)[D / 16]) {
+  f32x16 s;
 #pragma unroll
-  for (int x = 0; x < QT; ++x)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[x][r] = 0.f;
+  for (int r = 0; r < 16; ++r) s[r] = 0.f;
 #pragma unroll
   for (int st = 0; st < D / 16; ++st) {
     const bf16x8 k = decode_bf16(kw[st / 2][2 * (st % 2)], kw[st / 2][2 * (st % 2) + 1], ks);
-#pragma unroll
-    for (int x = 0; x < QT; ++x)
-      s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[x][st], s[x], 0, 0, 0);
+    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[st], s, 0, 0, 0);
   }
+  return s;
 }
 
 // The weights of one page (tokens t0 ..) and the running maximum and sum.
@@ -185,17 +194,17 @@ __device__ __forceinline__ void weigh_page(float c, int t0, int lim, bool masked
 #pragma unroll
   for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
   mx = halves_max(mx) * c;
-  const float m1 = fmaxf(tile.m, mx);
-  if (__builtin_amdgcn_ballot_w64(m1 > tile.m) != 0) {
-    // (-inf) - (-inf) never arises: m1 is above -inf where it rose
-    const float f = m1 > tile.m ? __builtin_amdgcn_exp2f(tile.m - m1) : 1.0f;
+  const bool rise = mx > tile.m + kRise;
+  if (__builtin_amdgcn_ballot_w64(rise) != 0) {
+    // (-inf) - (-inf) never arises: mx is above -inf where it rose
+    const float f = rise ? __builtin_amdgcn_exp2f(tile.m - mx) : 1.0f;
     tile.l *= f;
 #pragma unroll
     for (int cc = 0; cc < D / 32; ++cc) tile.o[cc] *= f;
-    tile.m = m1;
+    tile.m = rise ? mx : tile.m;
   }
   // a column that has met no token yet has m = -inf: weights 0
-  const float sub = m1 == kNegInf ? 0.f : m1 - kBias;
+  const float sub = tile.m == kNegInf ? 0.f : tile.m - kBias;
   float w[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -sub));
@@ -264,52 +273,53 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
   }
 }
 
-// WIDE: the four waves take different columns and the same pages; else they
-// share QT column tiles and take every fourth page, joined through LDS.
-template <int D, int QT, bool WIDE>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
+// One unit: sequence b, key/value head, column group (32 CW columns), split of
+// the tokens.
+template <int D, int CW, int KW>
+__global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kernel(AttnArgs a) {
   constexpr int REGS = D / 2;                      // accumulator registers of a tile
-  __shared__ float s_o[WIDE ? 1 : 2 * REGS * 64];
-  __shared__ float s_ml[WIDE ? 1 : 2 * 3 * 64];
+  constexpr int SLOTS = KW / 2 * CW;               // tiles handed over in one step
+  __shared__ float s_o[KW > 1 ? SLOTS * REGS * 64 : 1];
+  __shared__ float s_ml[KW > 1 ? SLOTS * 3 * 64 : 1];
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t unit = blockIdx.x;
-  const int group = (int)(unit % a.groups);
-  unit /= a.groups;
-  const int split = (int)(unit % a.splits);
-  unit /= a.splits;
-  const int hkv = (int)(unit % a.H);
-  const int64_t b = unit / a.H;
-  const int64_t c0 = WIDE ? ((int64_t)group * kAttnWaves + wave) * (32 * QT) : (int64_t)group * (32 * QT);
-  if (WIDE && c0 >= a.ncols) return;
+  const int cw = wave % CW, kw_id = wave / CW;
+  uint32_t unit = blockIdx.x;
+  if (a.groups > 1) {
+    // Workgroups go round robin to the 8 XCDs: give each XCD a run of units, so
+    // that the column groups of one head read its pages from one L2; longest
+    // column groups first (under the block mask later queries see more).
+    const uint32_t n8 = gridDim.x / 8, rest = gridDim.x % 8, x = unit % 8;
+    unit = x * n8 + min(x, rest) + unit / 8;
+  }
+  const int group = a.groups - 1 - (int)(unit % (uint32_t)a.groups);
+  unit /= (uint32_t)a.groups;
+  const int split = (int)(unit % (uint32_t)a.splits);
+  unit /= (uint32_t)a.splits;
+  const int hkv = (int)(unit % (uint32_t)a.H);
+  const int64_t b = unit / (uint32_t)a.H;
+  const int64_t c0 = ((int64_t)group * CW + cw) * 32;
   const int n = (int)cut_len(a.kv_lens[b], a.max_pages);
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
 
-  Column col[QT];
-  bf16x8 q[QT][D / 16];
-  Tile<D> tile[QT];
-  int max_lim = 0, min_lim = 0x7fffffff;
+  const Column col = column(a, b, c0 + (lane & 31), n, q_len);
+  bf16x8 q[D / 16];
+  load_query<D>(a, b, (int64_t)hkv * a.G + col.g, col, q);
+  const int max_lim = -wave_min_i(-col.lim);
+  const int min_lim = wave_min_i(col.lim);
+  Tile<D> tile;
 #pragma unroll
-  for (int x = 0; x < QT; ++x) {
-    col[x] = column(a, b, c0 + 32 * x + (lane & 31), n, q_len);
-    load_query<D>(a, b, (int64_t)hkv * a.G + col[x].g, col[x], q[x]);
-    max_lim = max(max_lim, col[x].lim);
-    min_lim = min(min_lim, col[x].lim);
+  for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) tile[x].o[c][r] = 0.f;
-    tile[x].m = kNegInf;
-    tile[x].l = 0.f;
-  }
-  max_lim = -wave_min_i(-max_lim);
-  min_lim = wave_min_i(min_lim);
+    for (int r = 0; r < 16; ++r) tile.o[c][r] = 0.f;
+  tile.m = kNegInf;
+  tile.l = 0.f;
   int E = kScaleMin;
-  const int64_t pages = (max_lim + kPage - 1) / kPage;
-  const int lo = (int)(pages * split / a.splits), hi = (int)(pages * (split + 1) / a.splits);
+  const int pages = (max_lim + kPage - 1) / kPage;
+  const int per = (pages + a.splits - 1) / a.splits;
+  const int lo = split * per, hi = min(lo + per, pages);
   const int32_t *row = a.table + b * a.table_stride;
-  constexpr int STEP = WIDE ? 1 : kAttnWaves;
-  int t = WIDE ? lo : lo + wave;
+  int t = lo + kw_id;
   if (t < hi) {
     // One buffer each for keys and values: the next page's keys are fetched
     // when this page's scores are done with them, its values after the
@@ -323,11 +333,10 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
     int ve = stored_exp(a.v_scale[ph]);
     for (;;) {
       const bool here = id >= 0;
-      const int next = t + STEP < hi ? t + STEP : t;
+      const int next = t + KW < hi ? t + KW : t;
       const int64_t id1 = page_of(row, next, a.num_pages);
       const int64_t ph1 = max(id1, (int64_t)0) * a.H + hkv;
-      f32x16 s[QT];
-      if (here) score_page<D, QT>(kw, ks, q, s);
+      f32x16 s = score_page<D>(kw, ks, q);
       load_pieces<D>(a.k, ph1, kw);
       const float ks1 = pow2(stored_exp(a.k_scale[ph1]));
       const int ve1 = stored_exp(a.v_scale[ph1]);
@@ -349,23 +358,17 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
           // the accumulators' unit 2^E follows the largest value scale
           const float f = __builtin_amdgcn_ldexpf(1.0f, E - ve);
 #pragma unroll
-          for (int x = 0; x < QT; ++x)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) tile[x].o[c] *= f;
+          for (int c = 0; c < D / 32; ++c) tile.o[c] *= f;
           E = ve;
         }
-        f16x8 p[QT][2];
-#pragma unroll
-        for (int x = 0; x < QT; ++x)
-          weigh_page<D>(a.c, t0, col[x].lim, t0 + kPage > min_lim, ve, E, s[x], tile[x], p[x]);
+        f16x8 p[2];
+        weigh_page<D>(a.c, t0, col.lim, t0 + kPage > min_lim, ve, E, s, tile, p);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const f16x8 v = decode_f16(vw[c][2 * e], vw[c][2 * e + 1]);
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-              tile[x].o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[x][e], tile[x].o[c], 0, 0, 0);
+            tile.o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[e], tile.o[c], 0, 0, 0);
           }
       }
       if (next == t) break;
@@ -376,67 +379,54 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
       ve = ve1;
     }
   }
-  if constexpr (!WIDE) {
-    // waves 2, 3 into 0, 1, then 1 into 0: every lane its own column's rows
+  if constexpr (KW > 1) {
+    // the upper half of the token waves into the lower, again and again: every
+    // lane its own column's rows
 #pragma unroll
-    for (int x = 0; x < QT; ++x) {
+    for (int step = KW / 2; step >= 1; step >>= 1) {
+      __syncthreads();
+      if (kw_id >= step && kw_id < 2 * step) {
+        const int slot = (kw_id - step) * CW + cw;
 #pragma unroll
-      for (int step = 2; step >= 1; step >>= 1) {
-        __syncthreads();
-        if (wave >= step && wave < 2 * step) {
-          const int slot = wave - step;
+        for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
+          for (int r = 0; r < 16; ++r) s_o[(slot * REGS + c * 16 + r) * 64 + lane] = tile.o[c][r];
+        s_ml[(slot * 3 + 0) * 64 + lane] = tile.m;
+        s_ml[(slot * 3 + 1) * 64 + lane] = tile.l;
+        s_ml[(slot * 3 + 2) * 64 + lane] = __int_as_float(E);
+      }
+      __syncthreads();
+      if (kw_id < step) {
+        const int slot = kw_id * CW + cw;
+        const float om = s_ml[(slot * 3 + 0) * 64 + lane], ol = s_ml[(slot * 3 + 1) * 64 + lane];
+        const int oe = __float_as_int(s_ml[(slot * 3 + 2) * 64 + lane]);
+        const float m1 = fmaxf(tile.m, om);
+        const float fa = tile.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(tile.m - m1);
+        const float fb = om == kNegInf ? 0.f : __builtin_amdgcn_exp2f(om - m1);
+        tile.l = tile.l * fa + ol * fb;
+        const int e1 = max(E, oe);
+        const float ga = fa * __builtin_amdgcn_ldexpf(1.0f, E - e1);
+        const float gb = fb * __builtin_amdgcn_ldexpf(1.0f, oe - e1);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s_o[(slot * REGS + c * 16 + r) * 64 + lane] = tile[x].o[c][r];
-          s_ml[(slot * 3 + 0) * 64 + lane] = tile[x].m;
-          s_ml[(slot * 3 + 1) * 64 + lane] = tile[x].l;
-          s_ml[(slot * 3 + 2) * 64 + lane] = __int_as_float(E);
-        }
-        __syncthreads();
-        if (wave < step) {
-          const float om = s_ml[(wave * 3 + 0) * 64 + lane], ol = s_ml[(wave * 3 + 1) * 64 + lane];
-          const int oe = __float_as_int(s_ml[(wave * 3 + 2) * 64 + lane]);
-          const float m1 = fmaxf(tile[x].m, om);
-          const float fa = tile[x].m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(tile[x].m - m1);
-          const float fb = om == kNegInf ? 0.f : __builtin_amdgcn_exp2f(om - m1);
-          // a NaN column stays NaN: its sum is
-          tile[x].l = tile[x].l * fa + ol * fb;
-          // units: the larger exponent for this column tile
-          const int e1 = max(E, oe);
-          const float ga = fa * __builtin_amdgcn_ldexpf(1.0f, E - e1);
-          const float gb = fb * __builtin_amdgcn_ldexpf(1.0f, oe - e1);
+        for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              tile[x].o[c][r] = tile[x].o[c][r] * ga + s_o[(wave * REGS + c * 16 + r) * 64 + lane] * gb;
-          tile[x].m = m1;
-          // the other tiles of this wave are still in the old unit
-#pragma unroll
-          for (int y = 0; y < QT; ++y)
-            if (y != x) {
-              const float f = __builtin_amdgcn_ldexpf(1.0f, E - e1);
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) tile[y].o[c] *= f;
-            }
-          E = e1;
-        }
+          for (int r = 0; r < 16; ++r)
+            tile.o[c][r] = tile.o[c][r] * ga + s_o[(slot * REGS + c * 16 + r) * 64 + lane] * gb;
+        tile.m = m1;
+        E = e1;
       }
     }
-    if (wave != 0) return;
+    if (kw_id != 0) return;
   }
-#pragma unroll
-  for (int x = 0; x < QT; ++x)
-    store_tile<D>(a, b, hkv, c0 + 32 * x + (lane & 31), split, col[x], tile[x], E);
+  store_tile<D>(a, b, hkv, c0 + (lane & 31), split, col, tile, E);
 }
 
 // One wave per query and head: joins the splits' parts in split order.
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
   if (row >= a.B * a.H * a.ncols) return;
   const int64_t c = row % a.ncols, bh = row / a.ncols;
   const int hkv = (int)(bh % a.H);
@@ -469,102 +459,139 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a
         (m + __builtin_amdgcn_logf(sum) - kBias) * kLn2;
 }
 
-// Attention weights: one workgroup per sequence and page.  Each wave takes every
-// fourth (head, column tile), recomputes S^T, and adds 2^(s - lse) into one
-// register per token of its lane's columns; the lanes and waves meet in LDS
-// once, in a fixed order.
+// Attention weights.  A wave holds the keys of two pages (64 tokens), decoded,
+// and walks the columns of its head: per 32 columns it recomputes S^T and adds
+// 2^(s - lse) into one register per token of its lane's columns.  The four
+// waves of a workgroup take neighbouring tokens and the same columns, whose
+// queries they read from the CU's cache.  A workgroup's columns are one part
+// (a share of a head's columns); lanes are folded at its end, and a second
+// kernel adds the parts of each token in order.
+constexpr int kWeightPages = 2;
+constexpr int kWeightTokens = kPage * kWeightPages * 4;     // of a workgroup
+
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void attention_weights_kernel(AttnArgs a) {
-  __shared__ float s_w[kAttnWaves * 64 * 17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int64_t t = blockIdx.x % a.max_pages, b = blockIdx.x / a.max_pages;
-  const int64_t n = cut_len(a.kv_lens[b], a.max_pages);
-  const int64_t t0 = t * kPage;
-  if (t0 >= n) return;
-  const int64_t id = page_of(a.table + b * a.table_stride, t, a.num_pages);
-  if (id < 0) return;
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kernel(AttnArgs a) {
+  constexpr int P = kWeightPages;
+  __shared__ float s_w[4][16][65];
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t unit = blockIdx.x;
+  const int part = (int)(unit % (uint32_t)a.parts);
+  unit /= (uint32_t)a.parts;
+  const int tg = (int)(unit % (uint32_t)a.token_groups);
+  const int64_t b = unit / (uint32_t)a.token_groups;
+  const int hkv = part % a.H, share = part / a.H;
+  const int n = (int)cut_len(a.kv_lens[b], a.max_pages);
+  const int t0 = tg * kWeightTokens + wave * (kPage * P);
+  if (tg * kWeightTokens >= n) return;                      // workgroup-uniform
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
+  const int32_t *row = a.table + b * a.table_stride;
   const int tiles = (a.ncols + 31) / 32;
-  float w[16];
+  const int u0 = (int)((int64_t)tiles * share / a.shares);
+  const int u1 = (int)((int64_t)tiles * (share + 1) / a.shares);
+
+  bf16x8 k[P][D / 16];
+  int end[P];                                               // tokens of page p that count
+  float w[P][16];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) w[r] = 0.f;
-  int held = -1;
-  bf16x8 k[D / 16];
-  for (int64_t u = wave; u < (int64_t)a.H * tiles; u += kAttnWaves) {
-    const int hkv = (int)(u / tiles);
-    const int64_t c0 = u % tiles * 32;
-    const Column col = column(a, b, c0 + (lane & 31), n, q_len);
-    if (__builtin_amdgcn_ballot_w64(col.lim > t0) == 0) continue;
-    if (hkv != held) {
-      held = hkv;
-      const int64_t ph = id * a.H + hkv;
-      const u32x4 *kp = reinterpret_cast<const u32x4 *>(a.k + ph * (kPage * D)) + lane;
-      const float ks = pow2(stored_exp(a.k_scale[ph]));
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const u32x4 x = kp[c * 64];
-        k[2 * c] = decode_bf16(x[0], x[1], ks);
-        k[2 * c + 1] = decode_bf16(x[2], x[3], ks);
-      }
-    }
-    const int64_t head = (int64_t)hkv * a.G + col.g;
-    bf16x8 q[D / 16];
-    load_query<D>(a, b, head, col, q);
-    f32x16 s;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = 0.f;
+  for (int p = 0; p < P; ++p) {
+    const int t = t0 / kPage + p;
+    const int64_t id = t0 + p * kPage < n ? page_of(row, t, a.num_pages) : -1;
+    end[p] = id < 0 ? 0 : n;
+    const int64_t ph = max(id, (int64_t)0) * a.H + hkv;
+    u32x4 kw[D / 32];
+    load_pieces<D>(a.k, ph, kw);
+    const float ks = pow2(stored_exp(a.k_scale[ph]));
 #pragma unroll
     for (int st = 0; st < D / 16; ++st)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[st], q[st], s, 0, 0, 0);
+      k[p][st] = decode_bf16(kw[st / 2][2 * (st % 2)], kw[st / 2][2 * (st % 2) + 1], ks);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) w[p][r] = 0.f;
+  }
+  for (int u = u0; u < u1; ++u) {
+    const Column col = column(a, b, (int64_t)u * 32 + (lane & 31), n, q_len);
+    const int64_t head = (int64_t)hkv * a.G + col.g;
     const float z = col.on ? a.lse[(b * a.H * a.G + head) * a.L + col.l] : kNegInf;
+    const int lim = z == kNegInf ? 0 : col.lim;             // a column that met nothing adds nothing
+    if (__builtin_amdgcn_ballot_w64(lim > t0) == 0) continue;
+    bf16x8 q[D / 16];
+    load_query<D>(a, b, head, col, q);
     const float sub = z * kLog2e;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const bool in = t0 + 8 * (r / 4) + 4 * h + r % 4 < col.lim && z != kNegInf;
-      w[r] += in ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
+    for (int p = 0; p < P; ++p) {
+      f32x16 s;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = 0.f;
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], q[st], s, 0, 0, 0);
+      const int left = min(lim, end[p]) - t0 - p * kPage - 4 * h;
+      if (__builtin_amdgcn_ballot_w64(left < kPage - 4 * h) == 0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) w[p][r] += __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          w[p][r] += 8 * (r / 4) + r % 4 < left ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
+      }
     }
   }
+  // fold the 32 columns of each half: lane (token, column half) of a page sums 16
 #pragma unroll
-  for (int r = 0; r < 16; ++r) s_w[(wave * 64 + lane) * 17 + r] = w[r];
-  __syncthreads();
-  // thread (token, eighth): 16 of the 128 (wave, lane) columns, then a fold
-  const int tok = threadIdx.x >> 3, part = threadIdx.x & 7;
-  const int r = tok / 8 * 4 + tok % 4, half = tok / 4 % 2;
-  float sum = 0.f;
+  for (int p = 0; p < P; ++p) {
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int j = part * 16 + i;                 // wave j / 32, column j % 32
-    sum += s_w[((j / 32) * 64 + half * 32 + j % 32) * 17 + r];
+    for (int r = 0; r < 16; ++r) s_w[wave][r][lane] = w[p][r];
+    __syncthreads();
+    const int tok = lane >> 1, r = tok / 8 * 4 + tok % 4, half = tok / 4 % 2;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += s_w[wave][r][half * 32 + (lane & 1) * 16 + i];
+    sum += __shfl_xor(sum, 1);
+    const int t = t0 + p * kPage + tok;
+    if ((lane & 1) == 0 && t < n)
+      a.part_w[((int64_t)part * a.B + b) * (a.max_pages * kPage) + t] = end[p] ? sum : 0.f;
   }
-  sum += __shfl_xor(sum, 1);
-  sum += __shfl_xor(sum, 2);
-  sum += __shfl_xor(sum, 4);
-  if (part == 0 && t0 + tok < n) a.weights[b * a.max_pages * kPage + t0 + tok] += sum;
+}
+
+__global__ __launch_bounds__(kJoinThreads) void attention_weights_join_kernel(AttnArgs a) {
+  const int64_t T = a.max_pages * kPage;
+  const int64_t blocks = (T + kJoinThreads - 1) / kJoinThreads;
+  const int64_t b = blockIdx.x / (uint32_t)blocks;
+  const int64_t t = (int64_t)(blockIdx.x % (uint32_t)blocks) * kJoinThreads + threadIdx.x;
+  if (t >= cut_len(a.kv_lens[b], a.max_pages)) return;
+  const float *p = a.part_w + b * T + t;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < a.parts; ++i) sum += p[(int64_t)i * a.B * T];
+  a.weights[b * T + t] += sum;
 }
 
 // ---------------------------------------------------------------- host side
 
 struct AttnPlan {
-  int qt;          // column tiles per wave
-  bool wide;
+  int cw, kw;      // column waves, token waves
   int groups, splits;
 };
 
-// Up to 64 columns: the waves of a workgroup share them and take turns at the
-// pages (more bytes in flight per column); above, each wave has its own
-// columns and the four read the same pages from the CU's cache.
+// 8 waves a workgroup (2 a SIMD at up to 256 registers; head_dim 256 needs 512,
+// 4 waves): as many column waves as there are column tiles, up to 4, the others
+// along the tokens.  Where the column groups alone give every CU two
+// workgroups, 4 column waves and no token waves.
 AttnPlan attn_plan(int64_t B, int64_t ncols, int64_t H, int64_t D, int64_t max_pages) {
+  const int64_t cus = device_cu_count(), tiles = std::max<int64_t>(1, (ncols + 31) / 32);
   AttnPlan p;
-  p.qt = D == 256 || ncols <= 32 ? 1 : 2;
-  p.wide = ncols > 32 * p.qt;
-  const int64_t per = 32 * p.qt * (p.wide ? kAttnWaves : 1);
-  p.groups = (int)((ncols + per - 1) / per);
-  // workgroups for two rounds of the CUs, of at least 4 pages (wide) or 2
-  // pages a wave
-  const int64_t want = 2LL * device_cu_count();
+  p.cw = tiles > 2 ? 4 : (int)tiles;
+  if (D == 256) p.cw = tiles > 1 ? 4 : 1;
+  p.groups = (int)((tiles + p.cw - 1) / p.cw);
   const int64_t units = std::max<int64_t>(1, B * H * p.groups);
+  p.kw = (D == 256 ? 4 : 8) / p.cw;
+  if (p.cw == 4 && units >= 2 * cus) p.kw = 1;
+  // split the tokens until every CU has its workgroups, with 2 pages or more
+  // per token wave and 4 or more per split
+  const int64_t want = (p.cw * p.kw == 8 ? 1 : 2) * cus;
   int64_t s = (want + units - 1) / units;
-  s = std::min<int64_t>(s, std::max<int64_t>(1, max_pages / (p.wide ? 4 : 2 * kAttnWaves)));
+  s = std::min<int64_t>(s, max_pages / std::max(2 * p.kw, 4));
   p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, s), 128);
   return p;
 }
@@ -622,7 +649,7 @@ AttnArgs attn_args(const dllm_kv_cache &c, const void *q, const int64_t *q_strid
   a.kv_lens = kv_lens;
   a.q_start = q_start;
   a.q_lens = q_lens;
-  a.block_len = block_len;
+  a.block_len = (uint32_t)block_len;
   a.B = B;
   a.H = c.kv_heads;
   a.G = (int)(q_heads / c.kv_heads);
@@ -634,18 +661,32 @@ AttnArgs attn_args(const dllm_kv_cache &c, const void *q, const int64_t *q_strid
 
 template <int D>
 void launch_attention(const AttnPlan &p, const AttnArgs &a, dim3 grid, hipStream_t s) {
-  const dim3 block(kAttnThreads);
-  if constexpr (D <= 128) {
-    if (p.qt == 2) {
-      if (p.wide) hipLaunchKernelGGL((attention_kernel<D, 2, true>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((attention_kernel<D, 2, false>), grid, block, 0, s, a);
-      return;
-    }
-    hipLaunchKernelGGL((attention_kernel<D, 1, false>), grid, block, 0, s, a);
+  if constexpr (D == 256) {
+    if (p.cw == 4) hipLaunchKernelGGL((attention_kernel<D, 4, 1>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<D, 1, 4>), grid, dim3(256), 0, s, a);
   } else {
-    if (p.wide) hipLaunchKernelGGL((attention_kernel<D, 1, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attention_kernel<D, 1, false>), grid, block, 0, s, a);
+    if (p.cw == 4 && p.kw == 1)
+      hipLaunchKernelGGL((attention_kernel<D, 4, 1>), grid, dim3(256), 0, s, a);
+    else if (p.cw == 4) hipLaunchKernelGGL((attention_kernel<D, 4, 2>), grid, dim3(512), 0, s, a);
+    else if (p.cw == 2) hipLaunchKernelGGL((attention_kernel<D, 2, 4>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<D, 1, 8>), grid, dim3(512), 0, s, a);
   }
+}
+
+// Parts of the attention weights: per key/value head, and shares of its columns
+// while that gives every CU four workgroups, of 4 or more column tiles.
+struct WeightPlan { int64_t token_groups; int shares; int64_t parts; };
+
+WeightPlan weight_plan(int64_t B, int64_t ncols, int64_t H, int64_t max_pages) {
+  WeightPlan p;
+  p.token_groups = (max_pages * kPage + kWeightTokens - 1) / kWeightTokens;
+  const int64_t tiles = std::max<int64_t>(1, (ncols + 31) / 32);
+  const int64_t units = std::max<int64_t>(1, B * H * p.token_groups);
+  int64_t s = (4LL * device_cu_count() + units - 1) / units;
+  s = std::min<int64_t>(s, tiles / 4);
+  p.shares = (int)std::max<int64_t>(1, s);
+  p.parts = H * p.shares;
+  return p;
 }
 
 }  // namespace
@@ -691,8 +732,7 @@ extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
   if (need > 0 && (uintptr_t)workspace % 16 != 0)
     return fail(DLLM_ERR_ARG, "%s: workspace must be 16-byte aligned", who);
   const int64_t wgs = B * a.H * p.groups * p.splits;
-  const int64_t limit = 0xffffffffLL / kAttnThreads;
-  if (wgs > limit || (rows + kAttnWaves - 1) / kAttnWaves > limit)
+  if (wgs > 0xffffffffLL / 512 || (rows + kJoinWaves - 1) / kJoinWaves > 0xffffffffLL / kJoinThreads)
     return fail(DLLM_ERR_UNSUPPORTED, "%s: too many queries in one call", who);
   a.out = (uint16_t *)out;
   a.out_vec = (uintptr_t)out % 8 == 0;
@@ -711,14 +751,22 @@ extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
   else launch_attention<256>(p, a, grid, stream);
   const int st = check_launch(who);
   if (st != DLLM_OK || p.splits == 1) return st;
-  const dim3 jgrid((uint32_t)((rows + kAttnWaves - 1) / kAttnWaves));
+  const dim3 jgrid((uint32_t)((rows + kJoinWaves - 1) / kJoinWaves));
   if (D == 64)
-    hipLaunchKernelGGL(attention_join_kernel<64>, jgrid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_join_kernel<64>, jgrid, dim3(kJoinThreads), 0, stream, a);
   else if (D == 128)
-    hipLaunchKernelGGL(attention_join_kernel<128>, jgrid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_join_kernel<128>, jgrid, dim3(kJoinThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL(attention_join_kernel<256>, jgrid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_join_kernel<256>, jgrid, dim3(kJoinThreads), 0, stream, a);
   return check_launch(who);
+}
+
+extern "C" size_t dllm_attention_weights_workspace_size(int64_t B, int64_t L, int64_t q_heads,
+                                                        int64_t kv_heads, int64_t max_pages) {
+  if (B < 0 || L < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0)
+    return 0;
+  const WeightPlan p = weight_plan(B, L * (q_heads / kv_heads), kv_heads, max_pages);
+  return (size_t)p.parts * B * max_pages * kPage * 4;
 }
 
 extern "C" int dllm_attention_weights(const dllm_kv_cache *cache, const void *q,
@@ -727,7 +775,8 @@ extern "C" int dllm_attention_weights(const dllm_kv_cache *cache, const void *q,
                                       int64_t max_pages, int64_t table_stride,
                                       const int32_t *kv_lens, const int32_t *q_start,
                                       const int32_t *q_lens, int64_t block_len, float scale,
-                                      const float *lse, float *weights, hipStream_t stream) {
+                                      const float *lse, float *weights, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream) {
   const char *who = "dllm_attention_weights";
   const int rc = check_attention(who, cache, q, q_strides, B, L, q_heads, page_table, max_pages,
                                  table_stride, kv_lens, block_len, scale);
@@ -736,17 +785,32 @@ extern "C" int dllm_attention_weights(const dllm_kv_cache *cache, const void *q,
   if (!lse || !weights) return fail(DLLM_ERR_ARG, "%s: lse and weights must be non-NULL", who);
   AttnArgs a = attn_args(*cache, q, q_strides, B, L, q_heads, page_table, max_pages, table_stride,
                          kv_lens, q_start, q_lens, block_len, scale);
+  const WeightPlan p = weight_plan(B, a.ncols, a.H, max_pages);
+  const int64_t limit = 0xffffffffLL / 256;
+  if (p.parts > limit / p.token_groups || B > limit / (p.parts * p.token_groups))
+    return fail(DLLM_ERR_UNSUPPORTED, "%s: too many pages in one call", who);
+  const size_t need = (size_t)p.parts * B * max_pages * kPage * 4;
+  if (!workspace || workspace_bytes < need)
+    return fail(DLLM_ERR_SHAPE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, need);
+  if ((uintptr_t)workspace % 16 != 0)
+    return fail(DLLM_ERR_ARG, "%s: workspace must be 16-byte aligned", who);
   a.lse = const_cast<float *>(lse);
   a.weights = weights;
-  const int64_t wgs = B * max_pages;
-  if (B > (0xffffffffLL / kAttnThreads) / max_pages)
-    return fail(DLLM_ERR_UNSUPPORTED, "%s: too many pages in one call", who);
-  const dim3 grid((uint32_t)wgs);
+  a.part_w = (float *)workspace;
+  a.parts = (int)p.parts;
+  a.shares = p.shares;
+  a.token_groups = (int)p.token_groups;
+  const dim3 grid((uint32_t)(B * p.token_groups * p.parts));
   if (cache->head_dim == 64)
-    hipLaunchKernelGGL(attention_weights_kernel<64>, grid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_weights_kernel<64>, grid, dim3(256), 0, stream, a);
   else if (cache->head_dim == 128)
-    hipLaunchKernelGGL(attention_weights_kernel<128>, grid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_weights_kernel<128>, grid, dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL(attention_weights_kernel<256>, grid, dim3(kAttnThreads), 0, stream, a);
+    hipLaunchKernelGGL(attention_weights_kernel<256>, grid, dim3(256), 0, stream, a);
+  const int st = check_launch(who);
+  if (st != DLLM_OK) return st;
+  const int64_t blocks = (max_pages * kPage + kJoinThreads - 1) / kJoinThreads;
+  hipLaunchKernelGGL(attention_weights_join_kernel, dim3((uint32_t)(B * blocks)),
+                     dim3(kJoinThreads), 0, stream, a);
   return check_launch(who);
 }

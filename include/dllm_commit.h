@@ -582,12 +582,19 @@ size_t dllm_block_attention_workspace_size(int64_t B, int64_t L, int64_t q_heads
  * cached token t received, sum over the queries and query heads of
  * exp(s_t - lse), for the same arguments and the lse of dllm_block_attention.
  * weights (B, 32 * max_pages) float32, read and written at t < kv_lens[b]
- * only; each entry is summed by one workgroup in a fixed order. */
+ * only; each entry is summed in a fixed order.  workspace: at least
+ * dllm_attention_weights_workspace_size() bytes, as in dllm_block_attention. */
 int dllm_attention_weights(const dllm_kv_cache *cache, const void *q, const int64_t *q_strides,
                            int64_t B, int64_t L, int64_t q_heads, const int32_t *page_table,
                            int64_t max_pages, int64_t table_stride, const int32_t *kv_lens,
                            const int32_t *q_start, const int32_t *q_lens, int64_t block_len,
-                           float scale, const float *lse, float *weights, hipStream_t stream);
+                           float scale, const float *lse, float *weights, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dllm_attention_weights needs on the current device.
+ * Returns 0 on bad arguments. */
+size_t dllm_attention_weights_workspace_size(int64_t B, int64_t L, int64_t q_heads,
+                                             int64_t kv_heads, int64_t max_pages);
 
 /* dllm_evict_select: which tokens of each cache to keep when it is cut down to
  * `budget`: with n = kv_lens[b], every token when n <= budget; else the first

@@ -116,10 +116,10 @@ def test_attention_refusals(lib):
                                         None)
 
     def weigh(c=None, q=fake, B=1, L=1, Hq=4, table=fake, pages=2, stride=2, lens=fake, bl=0,
-              scale=0.1, lse=fake, weights=fake):
+              scale=0.1, lse=fake, weights=fake, ws=fake, wsb=1 << 40):
         return lib.dllm_attention_weights(c if c is not None else _c(), q, S3, B, L, Hq, table,
                                           pages, stride, lens, None, None, bl, scale, lse, weights,
-                                          None)
+                                          ws, wsb, None)
 
     for f in (attend, weigh):
         for bad, status in BAD_CACHES:
@@ -133,6 +133,9 @@ def test_attention_refusals(lib):
         assert f(L=1 << 30) == -5
     assert attend(out=None) == -1 and attend(out=fake) == -1 and attend(out=P(513)) == -1
     assert weigh(weights=None) == -1
+    need = lib.dllm_attention_weights_workspace_size(1, 1, 4, 2, 2)
+    assert weigh(ws=None) == -3 and weigh(wsb=need - 1) == -3 and weigh(ws=P(260)) == -1
+    assert lib.dllm_attention_weights_workspace_size(1, 1, 4, 3, 2) == 0
     need = lib.dllm_block_attention_workspace_size(1, 1, 4, 2, 64, 1000)
     assert need > 0 and attend(pages=1000, stride=1000, ws=fake, wsb=need - 1) == -3
     assert attend(pages=1000, stride=1000, ws=P(260), wsb=need) == -1
