@@ -99,25 +99,26 @@ __device__ __forceinline__ Column column(const AttnArgs &a, int64_t b, int64_t c
 }
 
 // The column's query as D / 16 operand pieces: piece s of half h holds
-// channels 32 (s / 2) + 16 h + 8 (s % 2) .. + 7, as the keys' pieces do.
+// channels 32 (s / 2) + 16 h + 8 (s % 2) .. + 7, as the keys' pieces do.  A
+// column that is no real query reads some query's row (in bounds) and is
+// dropped later: columns do not mix.
 template <int D>
 __device__ __forceinline__ void load_query(const AttnArgs &a, int64_t b, int64_t head,
                                            const Column &col, bf16x8 (&q)[D / 16]) {
   const int h = (threadIdx.x & 63) >> 5;
   const uint16_t *row = a.q + b * a.qs[0] + col.l * a.qs[1] + head * a.qs[2];
+  if (a.vec) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      q[s] = *reinterpret_cast<const bf16x8 *>(row + 32 * (s / 2) + 16 * h + 8 * (s % 2));
+    return;
+  }
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
-    const int d = 32 * (s / 2) + 16 * h + 8 * (s % 2);
-    u32x4 w = {0, 0, 0, 0};
-    if (col.on) {
-      if (a.vec) {
-        w = *reinterpret_cast<const u32x4 *>(row + d);
-      } else {
+    const uint16_t *x = row + 32 * (s / 2) + 16 * h + 8 * (s % 2);
+    u32x4 w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = (uint32_t)row[d + 2 * e] | (uint32_t)row[d + 2 * e + 1] << 16;
-      }
-    }
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
     q[s] = __builtin_bit_cast(bf16x8, w);
   }
 }
@@ -203,17 +204,20 @@ __device__ __forceinline__ void weigh_page(float c, int t0, int lim, bool masked
     for (int cc = 0; cc < D / 32; ++cc) tile.o[cc] *= f;
     tile.m = rise ? mx : tile.m;
   }
+  // The page's value scale against the accumulators' unit goes into the
+  // exponent, as far as float32 reaches (2^-60), and out of the sum again.
+  const int de = max(ve - E, -60);
   // a column that has met no token yet has m = -inf: weights 0
-  const float sub = tile.m == kNegInf ? 0.f : tile.m - kBias;
+  const float sub = tile.m == kNegInf ? 0.f : tile.m - (kBias + (float)de);
   float w[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -sub));
   float l = 0.f;
 #pragma unroll
   for (int r = 0; r < 16; ++r) l += w[r];
-  tile.l += l;
-  if (ve < E) {
-    const float f = __builtin_amdgcn_ldexpf(1.0f, ve - E);
+  tile.l = fmaf(l, pow2(-de), tile.l);
+  if (ve - E < -60) {
+    const float f = __builtin_amdgcn_ldexpf(1.0f, ve - E + 60);
 #pragma unroll
     for (int r = 0; r < 16; ++r) w[r] *= f;
   }
@@ -319,64 +323,90 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
   const int per = (pages + a.splits - 1) / a.splits;
   const int lo = split * per, hi = min(lo + per, pages);
   const int32_t *row = a.table + b * a.table_stride;
-  int t = lo + kw_id;
-  if (t < hi) {
-    // One buffer each for keys and values: the next page's keys are fetched
-    // when this page's scores are done with them, its values after the
-    // products, so each load has the other half of a page's work to arrive.
-    u32x4 kw[D / 32], vw[D / 32];
-    int64_t id = page_of(row, t, a.num_pages);
-    int64_t ph = max(id, (int64_t)0) * a.H + hkv;     // a missing page reads page 0, unused
-    load_pieces<D>(a.k, ph, kw);
-    load_pieces<D>(a.v, ph, vw);
-    float ks = pow2(stored_exp(a.k_scale[ph]));
-    int ve = stored_exp(a.v_scale[ph]);
-    for (;;) {
-      const bool here = id >= 0;
-      const int next = t + KW < hi ? t + KW : t;
-      const int64_t id1 = page_of(row, next, a.num_pages);
-      const int64_t ph1 = max(id1, (int64_t)0) * a.H + hkv;
-      f32x16 s = score_page<D>(kw, ks, q);
-      load_pieces<D>(a.k, ph1, kw);
-      const float ks1 = pow2(stored_exp(a.k_scale[ph1]));
-      const int ve1 = stored_exp(a.v_scale[ph1]);
-      if (here) {
-        const int t0 = t * kPage;
-        if (t0 + kPage > n) {
-          // the cache ends inside this page: what lies behind may be any bits,
-          // and 0 * NaN is NaN, so the values there become 0
-          const int live = n - t0 - 4 * h;
+  // This wave's pages are lo + kw_id + KW i.  Lane j of the directory knows page
+  // i = 64 c + j of the current run of 64: no scalar load, with its wait for
+  // everything before it, stands between two pages.
+  int dir_at = -1, dir_ke = 0, dir_ve = 0;
+  int64_t dir_ph = 0;
+  const int count = (hi - lo - kw_id + KW - 1) / KW;
+  auto directory = [&](int i) {
+    const int t = lo + kw_id + (i + lane) * KW;
+    const int64_t id = i + lane < count ? page_of(row, t, a.num_pages) : -1;
+    dir_at = id < 0 ? -1 : t;
+    dir_ph = max(id, (int64_t)0) * a.H + hkv;         // a missing page reads page 0, unused
+    dir_ke = stored_exp(a.k_scale[dir_ph]);
+    dir_ve = stored_exp(a.v_scale[dir_ph]);
+    __builtin_amdgcn_s_waitcnt(0);
+  };
+  // Two page buffers in turn: a buffer's next keys are fetched when its scores
+  // are done with them, its next values after its products, so every load has
+  // about two pages' work to arrive.  Loads are unconditional, past the end
+  // they read page 0 or the last one again: a branch around them would make
+  // every wait one for all loads.
+  constexpr int NB = D == 256 ? 1 : 2;                // registers allow one at head_dim 256
+  u32x4 kw[NB][D / 32], vw[NB][D / 32];
+  int at[NB], ke[NB], ve[NB];                         // the buffers' pages (-1: none) and scales
+  int64_t ph[NB];
+  auto locate = [&](int x, int i) {
+    if ((i & 63) == 0) directory(i);
+    at[x] = __builtin_amdgcn_readlane(dir_at, i & 63);
+    ke[x] = __builtin_amdgcn_readlane(dir_ke, i & 63);
+    ve[x] = __builtin_amdgcn_readlane(dir_ve, i & 63);
+    ph[x] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)dir_ph, i & 63) |
+            (int64_t)__builtin_amdgcn_readlane((int)(dir_ph >> 32), i & 63) << 32;
+  };
+  auto page_step = [&](int x, int i) {
+    const int here = at[x], e_page = ve[x];
+    f32x16 s = score_page<D>(kw[x], pow2(ke[x]), q);
+    locate(x, i + NB);
+    load_pieces<D>(a.k, ph[x], kw[x]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (here >= 0) {
+      const int t0 = here * kPage;
+      if (t0 + kPage > n) {
+        // the cache ends inside this page: what lies behind may be any bits,
+        // and 0 * NaN is NaN, so the values there become 0
+        const int live = n - t0 - 4 * h;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int m = min(max(live - 8 * g, 0), 4);
-            const uint32_t keep = m == 4 ? ~0u : (1u << (8 * m)) - 1u;
+        for (int g = 0; g < 4; ++g) {
+          const int m = min(max(live - 8 * g, 0), 4);
+          const uint32_t keep = m == 4 ? ~0u : (1u << (8 * m)) - 1u;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) vw[c][g] &= keep;
-          }
+          for (int c = 0; c < D / 32; ++c) vw[x][c][g] &= keep;
         }
-        if (ve > E) {
-          // the accumulators' unit 2^E follows the largest value scale
-          const float f = __builtin_amdgcn_ldexpf(1.0f, E - ve);
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) tile.o[c] *= f;
-          E = ve;
-        }
-        f16x8 p[2];
-        weigh_page<D>(a.c, t0, col.lim, t0 + kPage > min_lim, ve, E, s, tile, p);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const f16x8 v = decode_f16(vw[c][2 * e], vw[c][2 * e + 1]);
-            tile.o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[e], tile.o[c], 0, 0, 0);
-          }
       }
-      if (next == t) break;
-      load_pieces<D>(a.v, ph1, vw);
-      t = next;
-      id = id1;
-      ks = ks1;
-      ve = ve1;
+      if (e_page > E) {
+        // the accumulators' unit 2^E follows the largest value scale
+        const float f = __builtin_amdgcn_ldexpf(1.0f, E - e_page);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tile.o[c] *= f;
+        E = e_page;
+      }
+      f16x8 p[2];
+      weigh_page<D>(a.c, t0, col.lim, t0 + kPage > min_lim, e_page, E, s, tile, p);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f16x8 v = decode_f16(vw[x][c][2 * e], vw[x][c][2 * e + 1]);
+          tile.o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[e], tile.o[c], 0, 0, 0);
+        }
+    }
+    load_pieces<D>(a.v, ph[x], vw[x]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (count > 0) {
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {
+      locate(x, x);
+      load_pieces<D>(a.k, ph[x], kw[x]);
+      __builtin_amdgcn_sched_barrier(0);
+      load_pieces<D>(a.v, ph[x], vw[x]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i = 0; i < count; i += NB) {
+#pragma unroll
+      for (int x = 0; x < NB; ++x) page_step(x, i + x);
     }
   }
   if constexpr (KW > 1) {
@@ -486,9 +516,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
   if (tg * kWeightTokens >= n) return;                      // workgroup-uniform
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
   const int32_t *row = a.table + b * a.table_stride;
-  const int tiles = (a.ncols + 31) / 32;
-  const int u0 = (int)((int64_t)tiles * share / a.shares);
-  const int u1 = (int)((int64_t)tiles * (share + 1) / a.shares);
+  // this part's column tiles, from the first query that sees token t0 to the
+  // last real one
+  const int tiles = (a.ncols + 31) / 32, per = (tiles + a.shares - 1) / a.shares;
+  int u0 = share * per;
+  const int64_t cols = max(q_len, (int64_t)0) * a.G;
+  const int u1 = (int)min((int64_t)min(u0 + per, tiles), (cols + 31) / 32);
+  if (a.block_len > 0) {
+    const uint32_t s = a.q_start ? (uint32_t)max(a.q_start[b], 0) : 0u;
+    const uint32_t from = (uint32_t)t0 / a.block_len * a.block_len;
+    if (from > s) u0 = (int)max((int64_t)u0, (int64_t)(from - s) * a.G / 32);
+  }
 
   bf16x8 k[P][D / 16];
   int end[P];                                               // tokens of page p that count
@@ -508,15 +546,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
 #pragma unroll
     for (int r = 0; r < 16; ++r) w[p][r] = 0.f;
   }
-  for (int u = u0; u < u1; ++u) {
+  // The next tile's queries are in flight while one is worked on.
+  struct Tile32 { bf16x8 q[D / 16]; float z; int lim; };
+  auto fetch = [&](int u, Tile32 &x) {
     const Column col = column(a, b, (int64_t)u * 32 + (lane & 31), n, q_len);
     const int64_t head = (int64_t)hkv * a.G + col.g;
-    const float z = col.on ? a.lse[(b * a.H * a.G + head) * a.L + col.l] : kNegInf;
-    const int lim = z == kNegInf ? 0 : col.lim;             // a column that met nothing adds nothing
-    if (__builtin_amdgcn_ballot_w64(lim > t0) == 0) continue;
-    bf16x8 q[D / 16];
-    load_query<D>(a, b, head, col, q);
-    const float sub = z * kLog2e;
+    x.z = col.on ? a.lse[(b * a.H * a.G + head) * a.L + col.l] : kNegInf;
+    x.lim = col.lim;
+    load_query<D>(a, b, head, col, x.q);
+  };
+  auto add = [&](const Tile32 &x) {
+    const int lim = x.z == kNegInf ? 0 : x.lim;             // a column that met nothing adds nothing
+    const float sub = x.z * kLog2e;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       f32x16 s;
@@ -524,7 +565,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
       for (int r = 0; r < 16; ++r) s[r] = 0.f;
 #pragma unroll
       for (int st = 0; st < D / 16; ++st)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], q[st], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], x.q[st], s, 0, 0, 0);
       const int left = min(lim, end[p]) - t0 - p * kPage - 4 * h;
       if (__builtin_amdgcn_ballot_w64(left < kPage - 4 * h) == 0) {
 #pragma unroll
@@ -534,6 +575,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
         for (int r = 0; r < 16; ++r)
           w[p][r] += 8 * (r / 4) + r % 4 < left ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
       }
+    }
+  };
+  if (u0 < u1) {
+    Tile32 x, y;
+    fetch(u0, x);
+    int u = u0;
+    for (; u + 2 < u1; u += 2) {
+      fetch(u + 1, y);
+      add(x);
+      fetch(u + 2, x);
+      add(y);
+    }
+    if (u + 1 < u1) {
+      fetch(u + 1, y);
+      add(x);
+      add(y);
+    } else {
+      add(x);
     }
   }
   // fold the 32 columns of each half: lane (token, column half) of a page sums 16
