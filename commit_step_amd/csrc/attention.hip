@@ -14,10 +14,11 @@
 // cache keeps a page's values in that token order (kv_dev.h): no weight
 // crosses lanes and no tile goes through LDS.
 //
-// p is biased by 2^14, so float16 keeps 11 bits of it down to 2^-28 and counts
-// weights down to 2^-39.  Pages whose value scale is smaller than the largest
-// seen (exponent E) have their p scaled by the difference, so the accumulator
-// is in units of 2^E.
+// A page's value scale 2^e goes into the exponents: w = 2^(s + e - m) multiplies
+// the codes, and the running reference m is that of s + e, what a token adds to
+// the output, so float16 keeps 11 bits of every w down to 2^-28 of the largest
+// and counts down to 2^-39 of it, however the scales differ.  m is an integer:
+// then every subtraction in an exponent and every rescaling is exact.
 //
 // A workgroup is CW column waves times KW token waves: the column waves read
 // the same pages (from the CU's cache), the token waves take turns at the pages
@@ -40,11 +41,15 @@ namespace {
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWaves = kJoinThreads / 64;
-constexpr float kBias = 14.0f;          // weights are held as 2^14 p
-// The maximum that weights are taken against follows the true one when it has
-// risen by more than this (base 2): weights stay below 2^15, within float16,
-// and the accumulators are rescaled rarely.
+constexpr float kBias = 14.0f;          // weights are held as 2^14 w
+// The reference m follows the maximum when that has risen by more than this
+// above it: weights stay below 2^15.5, within float16, and the accumulators are
+// rescaled rarely.
 constexpr float kRise = 1.0f;
+// Smallest exponent that goes into m: the sum of weights, which takes it out
+// again, stays within float32.  Pages of smaller values (below 2^-71) have
+// their weights scaled by the rest, within float16's 2^-20.
+constexpr int kMinExp = -80;
 
 struct AttnArgs {
   const uint16_t *q;
@@ -123,6 +128,27 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int64_t b, int64_t
   }
 }
 
+// Pieces s0 .. s0 + N - 1 of the column's query.
+template <int D, int N>
+__device__ __forceinline__ void load_pieces_of_query(const AttnArgs &a, int64_t b, int64_t head,
+                                                     const Column &col, int s0, bf16x8 (&q)[N]) {
+  const int h = (threadIdx.x & 63) >> 5;
+  const uint16_t *row = a.q + b * a.qs[0] + col.l * a.qs[1] + head * a.qs[2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int s = s0 + i;
+    const uint16_t *x = row + 32 * (s / 2) + 16 * h + 8 * (s % 2);
+    if (a.vec) {
+      q[i] = *reinterpret_cast<const bf16x8 *>(x);
+    } else {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
+      q[i] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+}
+
 // 8 codes times a power of two, exactly.
 __device__ __forceinline__ bf16x8 decode_bf16(uint32_t w0, uint32_t w1, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
@@ -162,7 +188,7 @@ __device__ __forceinline__ void load_pieces(const uint8_t *base, int64_t ph, u32
 template <int D>
 struct Tile {
   f32x16 o[D / 32];     // O^T: channel 32 c + 8 (r / 4) + 4 h + r % 4 of the lane's column
-  float m, l;           // base-2 maximum; biased sum over this half's tokens
+  float m, l;           // reference (an integer, -inf: nothing met); biased sum over this half
 };
 
 // S^T of one page: tokens x columns, in the keys' own unit.
@@ -180,61 +206,53 @@ __device__ __forceinline__ f32x16 score_page(const u32x4 (&kw)[D / 32], float ks
   return s;
 }
 
-// The weights of one page (tokens t0 ..) and the running maximum and sum.
+// The reference after a page's scores s with value exponent e, the accumulators
+// rescaled where it rose; returns what the scores' exponents subtract.
 template <int D>
-__device__ __forceinline__ void weigh_page(float c, int t0, int lim, bool masked, int ve, int E,
-                                           f32x16 &s, Tile<D> &tile, f16x8 (&p)[2]) {
-  const int h = (threadIdx.x & 63) >> 5;
-  if (masked) {
-    const int left = lim - t0 - 4 * h;
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (8 * (r / 4) + r % 4 >= left) s[r] = kNegInf;
-  }
+__device__ __forceinline__ float raise(float c, int e, const f32x16 &s, Tile<D> &tile) {
   float mx = s[0];
 #pragma unroll
   for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
-  mx = halves_max(mx) * c;
+  mx = fmaf(halves_max(mx), c, (float)e);
   const bool rise = mx > tile.m + kRise;
   if (__builtin_amdgcn_ballot_w64(rise) != 0) {
     // (-inf) - (-inf) never arises: mx is above -inf where it rose
-    const float f = rise ? __builtin_amdgcn_exp2f(tile.m - mx) : 1.0f;
+    const float m = __builtin_rintf(mx);
+    const float f = rise ? __builtin_amdgcn_exp2f(tile.m - m) : 1.0f;
     tile.l *= f;
 #pragma unroll
     for (int cc = 0; cc < D / 32; ++cc) tile.o[cc] *= f;
-    tile.m = rise ? mx : tile.m;
+    tile.m = rise ? m : tile.m;
   }
-  // The page's value scale against the accumulators' unit goes into the
-  // exponent, as far as float32 reaches (2^-60), and out of the sum again.
-  const int de = max(ve - E, -60);
   // a column that has met no token yet has m = -inf: weights 0
-  const float sub = tile.m == kNegInf ? 0.f : tile.m - (kBias + (float)de);
-  float w[16];
+  return tile.m == kNegInf ? 0.f : tile.m - (kBias + (float)e);
+}
+
+// log of the sum of exponentials, from the reference and the biased sum: the
+// sum's binary exponent joins the integers.  -inf for a column that met nothing.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  if (!(l > 0.f)) return m + l;
+  const int e = (int)(__float_as_uint(l) >> 23) - 127;
+  return ((m - kBias + (float)e) + __builtin_amdgcn_logf(__builtin_amdgcn_ldexpf(l, -e))) * kLn2;
+}
+
+template <int D>
+__device__ __forceinline__ void accumulate(const u32x4 (&vw)[D / 32], const f16x8 (&p)[2], Tile<D> &tile) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -sub));
-  float l = 0.f;
+  for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-  for (int r = 0; r < 16; ++r) l += w[r];
-  tile.l = fmaf(l, pow2(-de), tile.l);
-  if (ve - E < -60) {
-    const float f = __builtin_amdgcn_ldexpf(1.0f, ve - E + 60);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) w[r] *= f;
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int r = 0; r < 8; ++r) p[e][r] = (_Float16)w[8 * e + r];
+    for (int e = 0; e < 2; ++e)
+      tile.o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(decode_f16(vw[c][2 * e], vw[c][2 * e + 1]), p[e],
+                                                         tile.o[c], 0, 0, 0);
 }
 
 // Columns' results: the output itself, or this split's part.
 template <int D>
 __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv, int64_t c, int split,
-                                           const Column &col, const Tile<D> &t, int E) {
+                                           const Column &col, const Tile<D> &t) {
   const int h = (threadIdx.x & 63) >> 5;
   const float l = halves_sum(t.l);
   if (!col.on) return;
-  const float unit = pow2(E);
   if (a.splits == 1) {
     const float inv = l > 0.f ? 1.0f / l : (l == l ? 0.f : l);
     const int64_t head = (int64_t)hkv * a.G + col.g;
@@ -246,7 +264,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
         uint16_t y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          y[e] = __builtin_bit_cast(uint16_t, (__bf16)(t.o[cc][4 * g + e] * inv * unit));
+          y[e] = __builtin_bit_cast(uint16_t, (__bf16)(t.o[cc][4 * g + e] * inv));
         const int d = 32 * cc + 8 * g + 4 * h;
         if (a.out_vec) {
           *reinterpret_cast<uint2 *>(o + d) = __builtin_bit_cast(uint2, y);
@@ -257,7 +275,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
       }
     if (h == 0)
       a.lse[(b * a.H * a.G + head) * a.L + col.l] =
-          (t.m + __builtin_amdgcn_logf(l) - kBias) * kLn2;      // -inf when it met nothing
+          log_sum(t.m, l);
     return;
   }
   const int64_t row = ((b * a.H + hkv) * a.ncols + c) * a.splits + split;
@@ -268,7 +286,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
     for (int g = 0; g < 4; ++g) {
       f32x4 y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = t.o[cc][4 * g + e] * unit;
+      for (int e = 0; e < 4; ++e) y[e] = t.o[cc][4 * g + e];
       *reinterpret_cast<f32x4 *>(po + 32 * cc + 8 * g + 4 * h) = y;
     }
   if (h == 0) {
@@ -284,7 +302,7 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
   constexpr int REGS = D / 2;                      // accumulator registers of a tile
   constexpr int SLOTS = KW / 2 * CW;               // tiles handed over in one step
   __shared__ float s_o[KW > 1 ? SLOTS * REGS * 64 : 1];
-  __shared__ float s_ml[KW > 1 ? SLOTS * 3 * 64 : 1];
+  __shared__ float s_ml[KW > 1 ? SLOTS * 2 * 64 : 1];
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave % CW, kw_id = wave / CW;
@@ -318,7 +336,6 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
     for (int r = 0; r < 16; ++r) tile.o[c][r] = 0.f;
   tile.m = kNegInf;
   tile.l = 0.f;
-  int E = kScaleMin;
   const int pages = (max_lim + kPage - 1) / kPage;
   const int per = (pages + a.splits - 1) / a.splits;
   const int lo = split * per, hi = min(lo + per, pages);
@@ -338,9 +355,7 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
     dir_ve = stored_exp(a.v_scale[dir_ph]);
     __builtin_amdgcn_s_waitcnt(0);
   };
-  // Two page buffers in turn: a buffer's next keys are fetched when its scores
-  // are done with them, its next values after its products, so every load has
-  // about two pages' work to arrive.  Loads are unconditional, past the end
+  // Two page buffers in turn, fetched again when their page is done.  Loads are unconditional, past the end
   // they read page 0 or the last one again: a branch around them would make
   // every wait one for all loads.
   constexpr int NB = D == 256 ? 1 : 2;                // registers allow one at head_dim 256
@@ -355,14 +370,14 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
     ph[x] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)dir_ph, i & 63) |
             (int64_t)__builtin_amdgcn_readlane((int)(dir_ph >> 32), i & 63) << 32;
   };
-  auto page_step = [&](int x, int i) {
-    const int here = at[x], e_page = ve[x];
-    f32x16 s = score_page<D>(kw[x], pow2(ke[x]), q);
-    locate(x, i + NB);
-    load_pieces<D>(a.k, ph[x], kw[x]);
-    __builtin_amdgcn_sched_barrier(0);
+  // The page in buffer x, whose scores are in s; leaves the next page's there.
+  // Each matrix instruction of the next page's scores has two of this page's
+  // weights and its own operand's decoding beside it; the order is fixed, since
+  // the scheduler's own (all the decoding first) needs more registers.
+  auto page_step = [&](int x, int i, f32x16 &s) {
+    const int here = at[x], e_page = ve[x], y = (x + 1) % NB;
+    const int t0 = here * kPage;
     if (here >= 0) {
-      const int t0 = here * kPage;
       if (t0 + kPage > n) {
         // the cache ends inside this page: what lies behind may be any bits,
         // and 0 * NaN is NaN, so the values there become 0
@@ -375,25 +390,57 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
           for (int c = 0; c < D / 32; ++c) vw[x][c][g] &= keep;
         }
       }
-      if (e_page > E) {
-        // the accumulators' unit 2^E follows the largest value scale
-        const float f = __builtin_amdgcn_ldexpf(1.0f, E - e_page);
+      if (t0 + kPage > min_lim) {
+        const int left = col.lim - t0 - 4 * h;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) tile.o[c] *= f;
-        E = e_page;
+        for (int r = 0; r < 16; ++r)
+          if (8 * (r / 4) + r % 4 >= left) s[r] = kNegInf;
       }
-      f16x8 p[2];
-      weigh_page<D>(a.c, t0, col.lim, t0 + kPage > min_lim, e_page, E, s, tile, p);
+    } else {
+      // no page: weights 0, and values 0 (page 0's may be any bits)
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
+      for (int r = 0; r < 16; ++r) s[r] = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const f16x8 v = decode_f16(vw[x][c][2 * e], vw[x][c][2 * e + 1]);
-          tile.o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[e], tile.o[c], 0, 0, 0);
-        }
+      for (int c = 0; c < D / 32; ++c) vw[x][c] = u32x4{0, 0, 0, 0};
     }
+    const int e_in = max(e_page, kMinExp);
+    const float sub = raise<D>(a.c, e_in, s, tile);
+    f32x16 next;
+    f16x8 p[2];
+    float l = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) next[r] = 0.f;
+    constexpr int RS = 256 / D;                       // weights beside one matrix instruction
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      if constexpr (NB == 2) {
+        const bf16x8 k = decode_bf16(kw[y][st / 2][2 * (st % 2)], kw[y][st / 2][2 * (st % 2) + 1], pow2(ke[y]));
+        next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[st], next, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = st * RS; r < (st + 1) * RS; ++r) {
+        float w = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub));
+        l += w;
+        p[r / 8][r % 8] = (_Float16)w;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    tile.l = fmaf(l, pow2(-e_in), tile.l);
+    if (e_page < kMinExp) {
+      const _Float16 f = (_Float16)__builtin_amdgcn_ldexpf(1.0f, e_page - kMinExp);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) p[e] *= f;
+    }
+    accumulate<D>(vw[x], p, tile);
+    __builtin_amdgcn_sched_barrier(0);
+    // buffer x is free: its next page
+    locate(x, i + NB);
+    load_pieces<D>(a.k, ph[x], kw[x]);
+    __builtin_amdgcn_sched_barrier(0);
     load_pieces<D>(a.v, ph[x], vw[x]);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NB == 2) s = next;
+    else s = score_page<D>(kw[x], pow2(ke[x]), q);
   };
   if (count > 0) {
 #pragma unroll
@@ -404,9 +451,10 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
       load_pieces<D>(a.v, ph[x], vw[x]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    f32x16 s = score_page<D>(kw[0], pow2(ke[0]), q);
     for (int i = 0; i < count; i += NB) {
 #pragma unroll
-      for (int x = 0; x < NB; ++x) page_step(x, i + x);
+      for (int x = 0; x < NB; ++x) page_step(x, i + x, s);
     }
   }
   if constexpr (KW > 1) {
@@ -421,34 +469,28 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
           for (int r = 0; r < 16; ++r) s_o[(slot * REGS + c * 16 + r) * 64 + lane] = tile.o[c][r];
-        s_ml[(slot * 3 + 0) * 64 + lane] = tile.m;
-        s_ml[(slot * 3 + 1) * 64 + lane] = tile.l;
-        s_ml[(slot * 3 + 2) * 64 + lane] = __int_as_float(E);
+        s_ml[(slot * 2 + 0) * 64 + lane] = tile.m;
+        s_ml[(slot * 2 + 1) * 64 + lane] = tile.l;
       }
       __syncthreads();
       if (kw_id < step) {
         const int slot = kw_id * CW + cw;
-        const float om = s_ml[(slot * 3 + 0) * 64 + lane], ol = s_ml[(slot * 3 + 1) * 64 + lane];
-        const int oe = __float_as_int(s_ml[(slot * 3 + 2) * 64 + lane]);
+        const float om = s_ml[(slot * 2 + 0) * 64 + lane], ol = s_ml[(slot * 2 + 1) * 64 + lane];
         const float m1 = fmaxf(tile.m, om);
         const float fa = tile.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(tile.m - m1);
         const float fb = om == kNegInf ? 0.f : __builtin_amdgcn_exp2f(om - m1);
         tile.l = tile.l * fa + ol * fb;
-        const int e1 = max(E, oe);
-        const float ga = fa * __builtin_amdgcn_ldexpf(1.0f, E - e1);
-        const float gb = fb * __builtin_amdgcn_ldexpf(1.0f, oe - e1);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            tile.o[c][r] = tile.o[c][r] * ga + s_o[(slot * REGS + c * 16 + r) * 64 + lane] * gb;
+            tile.o[c][r] = tile.o[c][r] * fa + s_o[(slot * REGS + c * 16 + r) * 64 + lane] * fb;
         tile.m = m1;
-        E = e1;
       }
     }
     if (kw_id != 0) return;
   }
-  store_tile<D>(a, b, hkv, c0 + (lane & 31), split, col, tile, E);
+  store_tile<D>(a, b, hkv, c0 + (lane & 31), split, col, tile);
 }
 
 // One wave per query and head: joins the splits' parts in split order.
@@ -486,16 +528,15 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   for (int e = 0; e < PER; ++e) o[e] = __builtin_bit_cast(uint16_t, (__bf16)(acc[e] * inv));
   if (lane == 0)
     a.lse[(b * a.H * a.G + head) * a.L + l] =
-        (m + __builtin_amdgcn_logf(sum) - kBias) * kLn2;
+        log_sum(m, sum);
 }
 
 // Attention weights.  A wave holds the keys of two pages (64 tokens), decoded,
 // and walks the columns of its head: per 32 columns it recomputes S^T and adds
 // 2^(s - lse) into one register per token of its lane's columns.  The four
-// waves of a workgroup take neighbouring tokens and the same columns, whose
-// queries they read from the CU's cache.  A workgroup's columns are one part
-// (a share of a head's columns); lanes are folded at its end, and a second
-// kernel adds the parts of each token in order.
+// waves of a workgroup take neighbouring tokens and the same columns.  A
+// workgroup's columns are one part (a share of a head's columns); lanes are
+// folded at its end, and a second kernel adds the parts of each token in order.
 constexpr int kWeightPages = 2;
 constexpr int kWeightTokens = kPage * kWeightPages * 4;     // of a workgroup
 
@@ -503,6 +544,7 @@ template <int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kernel(AttnArgs a) {
   constexpr int P = kWeightPages;
   __shared__ float s_w[4][16][65];
+  __shared__ u32x4 s_q[2][D / 16][64];
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t unit = blockIdx.x;
@@ -516,15 +558,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
   if (tg * kWeightTokens >= n) return;                      // workgroup-uniform
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
   const int32_t *row = a.table + b * a.table_stride;
-  // this part's column tiles, from the first query that sees token t0 to the
-  // last real one
+  // this part's column tiles, from the first query that sees the workgroup's
+  // first token to the last real one
   const int tiles = (a.ncols + 31) / 32, per = (tiles + a.shares - 1) / a.shares;
   int u0 = share * per;
   const int64_t cols = max(q_len, (int64_t)0) * a.G;
   const int u1 = (int)min((int64_t)min(u0 + per, tiles), (cols + 31) / 32);
   if (a.block_len > 0) {
     const uint32_t s = a.q_start ? (uint32_t)max(a.q_start[b], 0) : 0u;
-    const uint32_t from = (uint32_t)t0 / a.block_len * a.block_len;
+    const uint32_t from = (uint32_t)(tg * kWeightTokens) / a.block_len * a.block_len;
     if (from > s) u0 = (int)max((int64_t)u0, (int64_t)(from - s) * a.G / 32);
   }
 
@@ -546,54 +588,92 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
 #pragma unroll
     for (int r = 0; r < 16; ++r) w[p][r] = 0.f;
   }
-  // The next tile's queries are in flight while one is worked on.
-  struct Tile32 { bf16x8 q[D / 16]; float z; int lim; };
-  auto fetch = [&](int u, Tile32 &x) {
-    const Column col = column(a, b, (int64_t)u * 32 + (lane & 31), n, q_len);
+  // The four waves share the tiles' queries through LDS, each fetching a
+  // quarter of the next tile's while one is worked on, and the scores of one
+  // tile become weights while the matrix instructions compute the next one's.
+  struct Cols { float z; int lim; };                        // a tile's lse and limits, as loaded
+  constexpr int QW = D / 64;                                // pieces a wave fetches
+  bf16x8 part_q[QW];
+  auto fetch = [&](int u, Cols &x) {
+    const Column col = column(a, b, (int64_t)min(u, u1 - 1) * 32 + (lane & 31), n, q_len);
     const int64_t head = (int64_t)hkv * a.G + col.g;
-    x.z = col.on ? a.lse[(b * a.H * a.G + head) * a.L + col.l] : kNegInf;
+    x.z = a.lse[(b * a.H * a.G + head) * a.L + col.l];
     x.lim = col.lim;
-    load_query<D>(a, b, head, col, x.q);
+    load_pieces_of_query<D, QW>(a, b, head, col, wave * QW, part_q);
   };
-  auto add = [&](const Tile32 &x) {
-    const int lim = x.z == kNegInf ? 0 : x.lim;             // a column that met nothing adds nothing
+  auto publish = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < QW; ++i) s_q[u & 1][wave * QW + i][lane] = __builtin_bit_cast(u32x4, part_q[i]);
+  };
+  auto score = [&](const bf16x8 (&kk)[D / 16], const bf16x8 (&q)[D / 16]) {
+    f32x16 s;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = 0.f;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st)
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk[st], q[st], s, 0, 0, 0);
+    return s;
+  };
+  auto weigh = [&](int p, const f32x16 &s, const Cols &x) {
+    const int lim = x.z == kNegInf ? 0 : x.lim;             // met nothing: adds nothing
+    const int left = min(lim, end[p]) - t0 - p * kPage - 4 * h;
     const float sub = x.z * kLog2e;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      f32x16 s;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = 0.f;
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], x.q[st], s, 0, 0, 0);
-      const int left = min(lim, end[p]) - t0 - p * kPage - 4 * h;
-      if (__builtin_amdgcn_ballot_w64(left < kPage - 4 * h) == 0) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) w[p][r] += __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          w[p][r] += 8 * (r / 4) + r % 4 < left ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
-      }
-    }
+    for (int r = 0; r < 16; ++r)
+      w[p][r] += 8 * (r / 4) + r % 4 < left ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
   };
   if (u0 < u1) {
-    Tile32 x, y;
-    fetch(u0, x);
-    int u = u0;
-    for (; u + 2 < u1; u += 2) {
-      fetch(u + 1, y);
-      add(x);
-      fetch(u + 2, x);
-      add(y);
+    Cols xa, xb;
+    f32x16 s[P];
+    bf16x8 q[D / 16];
+    fetch(u0, xa);
+    publish(u0);
+    __syncthreads();
+    fetch(u0 + 1, xb);
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, s_q[u0 & 1][st][lane]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) s[p] = score(k[p], q);
+    for (int u = u0; u + 1 < u1; ++u) {
+      // s: the scores of tile u, xa its columns; part_q, xb: tile u + 1's
+      publish(u + 1);
+      __syncthreads();
+      Cols xc;
+      fetch(u + 2, xc);
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st)
+        q[st] = __builtin_bit_cast(bf16x8, s_q[(u + 1) & 1][st][lane]);
+      // a whole tile: every column sees every token of both pages
+      const float sub = xa.z * kLog2e;
+      bool whole = __builtin_amdgcn_ballot_w64(xa.z == kNegInf) == 0;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        whole = whole && __builtin_amdgcn_ballot_w64(min(xa.lim, end[p]) - t0 < (p + 1) * kPage) == 0;
+      if (whole) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const f32x16 next = score(k[p], q);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) w[p][r] += __builtin_amdgcn_exp2f(fmaf(s[p][r], a.c, -sub));
+#pragma unroll
+          for (int st = 0; st < D / 16; ++st) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // a matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x002 | 0x400, 768 / D, 0);  // then vector work
+          }
+          s[p] = next;
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          weigh(p, s[p], xa);
+          s[p] = score(k[p], q);
+        }
+      }
+      xa = xb;
+      xb = xc;
     }
-    if (u + 1 < u1) {
-      fetch(u + 1, y);
-      add(x);
-      add(y);
-    } else {
-      add(x);
-    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) weigh(p, s[p], xa);
   }
   // fold the 32 columns of each half: lane (token, column half) of a page sums 16
 #pragma unroll
