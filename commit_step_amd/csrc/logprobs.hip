@@ -1,8 +1,8 @@
 // dllm_token_logprobs and dllm_token_logprobs_grad: scores of given tokens.
 //
 // Forward, per scored position: one pass over V logits keeps, per wave, the
-// running maximum M, z- and S of token_stats_dev.h (chunk_update), and a
-// sorted list of the K largest logits.  Then
+// running maximum M, z- and S of token_stats_dev.h (chunk_update), and the
+// candidates for the K largest logits.  Then
 //   log p_t = (x_t - M) / T - log1p(z-),   H = log1p(z-) - ln2 S / (1 + z-).
 // Bound by reading the logits once from HBM.
 //
@@ -65,119 +65,141 @@ __device__ __forceinline__ bool suppressed(const A &a, int64_t v) {
 }
 
 // ---------------------------------------------------------------- the K largest
+// Every wave collects candidates, elements that reach a bound below which the
+// row's K largest cannot lie, unsorted in LDS; the few that are left at the end
+// are ranked by counting.  The bound is the K-th largest of 64 groups' maxima
+// (4 lanes each, over everything they have seen): K elements reach it.  It is
+// taken in iterations 0, 1, 3 and 7 (one barrier each), so the candidates of a
+// row are about K (2 + log2 of its iterations).  A sorted list per wave with
+// one insertion after another measured 32 us for one token's 20 alternatives
+// over 126464 ids, this 14 us; 8 us without alternatives.
+//
+// A candidate is a 64-bit key: the value's order-preserving bits, best first,
+// then the id, so ascending keys are decreasing logits, equal ones by id.
 
-// A wave's K largest logits: lane i holds the i-th best (value, id), equal
-// values by lower id, lanes past the last entry (-inf, kIdxNone).  tau is the
-// K-th value (-inf until K entries are held).
-struct TopList {
-  float v;
-  int id;
-  float tau;
+constexpr int kCap = 256;            // candidates of a wave
+
+__device__ __forceinline__ uint64_t top_key(float v, int id) {
+  return ((uint64_t)conf_key(v) << 32) | (uint32_t)id;
+}
+
+// The K-th largest of the 64 groups' maxima (-inf when fewer groups hold
+// anything).  Every thread calls it; gm is one of two buffers used in turn.
+__device__ __forceinline__ float group_bound(float tmax, int K, float *gm) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float q = fmaxf(tmax, dpp_f<kQuadSwap1>(tmax, tmax));
+  q = fmaxf(q, dpp_f<kQuadSwap2>(q, q));
+  if ((lane & 3) == 0) gm[wave * 16 + (lane >> 2)] = q;
+  __syncthreads();
+  const float v = gm[lane];
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < 64; j += 4) {
+    const float4 o = *reinterpret_cast<const float4 *>(gm + j);
+    above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+  }
+  // the smallest value with fewer than K above it
+  return -wave_max(above < K ? -v : -kInf);
+}
+
+// A wave's candidates: n (wave-uniform) keys in buf, and the key that a new one
+// has to stay below (kNoKey until a full buffer was cut to its K best).
+struct Candidates {
+  uint64_t *buf;
+  int n;
+  uint64_t kth;
 };
 
-constexpr int kWaveShr1 = 0x138;   // DPP: every lane takes its lower neighbour's value
-
-// Insert a wave-uniform (v, id), v > -inf.
-__device__ __forceinline__ void top_insert(TopList &t, int K, float v, int id) {
-  const bool ahead = t.v > v || (t.v == v && t.id < id);
-  const int pos = __builtin_popcountll(__builtin_amdgcn_ballot_w64(ahead));
-  if (pos >= K) return;
+// Cut the wave's buffer to its K smallest keys.
+__device__ __forceinline__ void cut_to_best(Candidates &c, int K) {
   const int lane = threadIdx.x & 63;
-  const float pv = dpp_f<kWaveShr1>(t.v, t.v);
-  const int pi = dpp_i<kWaveShr1>(t.id, t.id);
-  t.v = lane < pos ? t.v : lane == pos ? v : pv;
-  t.id = lane < pos ? t.id : lane == pos ? id : pi;
-  t.tau = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(t.v), K - 1));
+  uint64_t k[kCap / 64];
+#pragma unroll
+  for (int j = 0; j < kCap / 64; ++j) k[j] = lane + 64 * j < c.n ? c.buf[lane + 64 * j] : kNoKey;
+  uint64_t mine = kNoKey;
+  for (int i = 0; i < K; ++i) {
+    uint64_t m = k[0];
+#pragma unroll
+    for (int j = 1; j < kCap / 64; ++j) m = k[j] < m ? k[j] : m;
+    const uint64_t best = wave_min_u64(m);
+    if (lane == i) mine = best;
+#pragma unroll
+    for (int j = 0; j < kCap / 64; ++j) k[j] = k[j] == best ? kNoKey : k[j];
+    c.kth = best;
+  }
+  // the reads above are complete in every lane: a wave's LDS operations are in order
+  if (lane < K) c.buf[lane] = mine;
+  c.n = K;
+}
+
+// Lanes with `pass` offer (v, id).
+__device__ __forceinline__ void offer(Candidates &c, int K, bool pass, float v, int id) {
+  const uint64_t key = top_key(v, id);
+  uint64_t m = __builtin_amdgcn_ballot_w64(pass && key < c.kth);
+  if (m == 0) return;
+  if (c.n + __builtin_popcountll(m) > kCap) {
+    cut_to_best(c, K);
+    m = __builtin_amdgcn_ballot_w64(pass && key < c.kth);
+  }
+  const int lane = threadIdx.x & 63;
+  const int at = c.n + __builtin_popcountll(m & ((1ull << lane) - 1ull));
+  if ((m >> lane) & 1ull) c.buf[at] = key;
+  c.n += __builtin_popcountll(m);
+}
+
+// The smallest value that is a candidate: the bound itself where elements equal
+// to it count (a chunk that is part of the bound, or whose ids come before
+// others'), else the next float (ids ascend from chunk to chunk, and K elements
+// of lower id reach the bound); never -inf.
+__device__ __forceinline__ float least_candidate(float bound, bool equal) {
+  if (bound == -kInf) return -3.40282347e38f;
+  if (equal) return bound;
+  if (bound == 0.f) return 1.4e-45f;
+  const uint32_t u = __float_as_uint(bound);
+  return __uint_as_float(bound > 0.f ? u + 1u : u - 1u);      // above +inf: NaN, which nothing reaches
 }
 
 // One chunk of the sweep: every lane holds U loads of VEC elements, element j
-// of load k of lane ln at id idx_of(k, j, ln).  ORDERED: ids ascend from chunk
-// to chunk, so an element equal to tau comes behind the list's.  A chunk none
-// of whose lanes exceeds tau costs one ballot.  When K or more lanes exceed
-// it, the K-th largest of the lanes' maxima bounds the K-th largest element
-// from below, and only elements that reach it are inserted: without it the
-// first chunk would insert every new maximum in turn.
-template <int U, int VEC, bool ORDERED, typename IdxF>
-__device__ __forceinline__ void top_update(TopList &t, int K, const float (&x)[U * VEC],
-                                           IdxF idx_of) {
-  const int lane = threadIdx.x & 63;
-  float lm[U], cm = -kInf;
+// of load k at id idx_of(k, j); those of at least `least` are offered, the
+// lanes' first ones together, then their second ones.
+template <int U, int VEC, typename IdxF>
+__device__ __forceinline__ void collect(Candidates &c, int K, const float (&x)[U * VEC], float least,
+                                        IdxF idx_of) {
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    lm[k] = x[k * VEC];
+    uint32_t bits = 0;
 #pragma unroll
-    for (int j = 1; j < VEC; ++j) lm[k] = fmaxf(lm[k], x[k * VEC + j]);
-    cm = fmaxf(cm, lm[k]);
-  }
-  const uint64_t hot = __builtin_amdgcn_ballot_w64(ORDERED ? cm > t.tau : cm >= t.tau);
-  if (hot == 0) return;
-  float least = -kInf;
-  if (__builtin_popcountll(hot) >= K) {
-    int rank = 0;
+    for (int j = 0; j < VEC; ++j) bits |= x[k * VEC + j] >= least ? 1u << j : 0u;
+    while (__builtin_amdgcn_ballot_w64(bits != 0) != 0) {
+      const int j = bits ? __builtin_ctz(bits) : 0;
+      float v = x[k * VEC];
 #pragma unroll
-    for (int q = 0; q < 64; ++q) {
-      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cm), q));
-      rank += o > cm || (o == cm && q < lane);
-    }
-    const uint64_t at = __builtin_amdgcn_ballot_w64(rank == K - 1);
-    // a NaN maximum (a lane of NaNs) ranks nowhere exactly; then no bound
-    if (at) {
-      const int ln = __builtin_ctzll(at);
-      const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cm), ln));
-      least = b == b ? b : -kInf;
-    }
-  }
-  auto pass = [&](float v) {
-    return (ORDERED ? v > t.tau : v >= t.tau) && v >= least && v > -kInf;
-  };
-#pragma unroll
-  for (int k = 0; k < U; ++k) {
-    uint64_t lanes = __builtin_amdgcn_ballot_w64(pass(lm[k]));
-    while (lanes) {
-      const int ln = __builtin_ctzll(lanes);
-      lanes &= lanes - 1;
-      // the lane's VEC elements, one per lane
-      int w = __float_as_int(-kInf);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int e = __builtin_amdgcn_readlane(__float_as_int(x[k * VEC + j]), ln);
-        w = lane == j ? e : w;
-      }
-      const float wv = __int_as_float(w);
-      uint64_t m = __builtin_amdgcn_ballot_w64(pass(wv));
-      while (m) {
-        const int j = __builtin_ctzll(m);
-        m &= m - 1;
-        const float v = __int_as_float(__builtin_amdgcn_readlane(w, j));
-        top_insert(t, K, v, idx_of(k, j, ln));
-      }
+      for (int e = 1; e < VEC; ++e) v = j == e ? x[k * VEC + e] : v;
+      offer(c, K, bits != 0, v, idx_of(k, j));
+      bits &= bits - 1u;
     }
   }
 }
 
-// Order-preserving key of a list entry: ascending keys are the list's order.
-__device__ __forceinline__ uint64_t top_key(float v, int id) {
-  return id == kIdxNone ? kNoKey : ((uint64_t)conf_key(v) << 32) | (uint32_t)id;
-}
-
-// The K smallest of the n keys in LDS (distinct but for kNoKey), ranked by
-// counting, into out[0 .. K-1]; every thread of the workgroup calls it.  Lists
-// of K sorted keys: the smallest K-th entry of any list bounds the result, so
-// only the keys up to it are ranked (about K of a long row's slices).
-__device__ __forceinline__ void select_keys(const uint64_t *keys, int n, int K, uint64_t *cand,
-                                            int *n_cand, uint64_t *bound, uint64_t *out) {
+// The K smallest of the workgroup's keys, each thread holding N (kNoKey: none),
+// in order into out[0 .. K-1] (kNoKey past the last): the K-th best group's
+// value bounds them again, and what reaches it is ranked by counting.  Every
+// thread calls it; cand has room for all keys.
+template <int N>
+__device__ __forceinline__ void select_keys(const uint64_t (&key)[N], int K, float *gm, uint64_t *cand,
+                                            int *n_cand, uint64_t *out) {
   const int tid = threadIdx.x;
-  if (tid == 0) { *n_cand = 0; *bound = kNoKey; }
+  float best = -kInf;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (key[i] != kNoKey) best = fmaxf(best, conf_from_key((uint32_t)(key[i] >> 32)));
+  if (tid == 0) *n_cand = 0;
   if (tid < K) out[tid] = kNoKey;
-  __syncthreads();
-  for (int i = K - 1 + tid * K; i < n; i += kTopThreads * K)
-    atomicMin((unsigned long long *)bound, (unsigned long long)keys[i]);
-  __syncthreads();
-  const uint64_t b = *bound;
-  for (int i = tid; i < n; i += kTopThreads) {
-    const uint64_t k = keys[i];
-    if (k <= b && k != kNoKey) cand[atomicAdd(n_cand, 1)] = k;
-  }
+  const float bound = group_bound(best, K, gm);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (key[i] != kNoKey && conf_from_key((uint32_t)(key[i] >> 32)) >= bound)
+      cand[atomicAdd(n_cand, 1)] = key[i];
   __syncthreads();
   const int m = *n_cand;
   for (int i = tid; i < m; i += kTopThreads) {
@@ -260,15 +282,17 @@ __device__ RowSums plain_row(const LogprobArgs &a, const T *row, float *fs, int 
 
 // ---------------------------------------------------------------- forward
 
-template <typename T>
-__global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kTopThreads, 4) void logprob_kernel(LogprobArgs a) {
   using E = ElemT<T>;
   constexpr int VEC = E::VEC, U = E::U, CH = U * VEC, STEP = kTopThreads * CH;
-  constexpr int kKeys = kMaxTopSlices * DLLM_MAX_TOP;
+  constexpr int kKeys = kMaxTopSlices * DLLM_MAX_TOP;         // of a row's slices
+  static_assert(kKeys >= kTopWaves * kCap, "room for every wave's candidates");
   __shared__ Partial wave_parts[kTopWaves];
-  __shared__ uint64_t keys[kKeys], cand[kKeys];
+  __shared__ uint64_t wave_cand[TOP ? kTopWaves : 1][kCap];
+  __shared__ uint64_t cand[TOP ? kKeys : kTopThreads];
   __shared__ uint64_t best[DLLM_MAX_TOP];
-  __shared__ uint64_t s_bound;
+  __shared__ __align__(16) float gm[2][64];
   __shared__ int s_ncand, s_last;
   __shared__ Partial s_part;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -299,7 +323,8 @@ __global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
   st.c = a.c;
   st.M = -kInf; st.R = -kInf; st.idx = kIdxNone; st.zx = 0.f; st.Sx = 0.f; st.z = 0.f; st.S = 0.f;
   st.sb = -kInf; st.ib = kIdxNone; st.xb = -kInf; st.m2 = -kInf; st.m2x = -kInf;
-  TopList tl{-kInf, kIdxNone, -kInf};
+  Candidates tc{TOP ? wave_cand[wave] : nullptr, 0, kNoKey};
+  float tmax = -kInf, bound = -kInf;
   int sp = 0;
 
   // The slice's 16-byte-aligned body [blo, bhi); its head and tail, fewer than
@@ -308,19 +333,37 @@ __global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
   const int64_t blo = min(lo + (int64_t)(((16u - mis) & 15u) / sizeof(T)), hi);
   const int64_t bhi = blo + (hi - blo) / VEC * VEC;
 
-  for (int64_t base = blo; base < bhi; base += STEP) {
-    float x[CH];
-    uint4 r[U];
+  // The next iteration's loads are in flight while one is reduced.  A lane past
+  // the end reads the body's first word (in bounds, its value unused).
+  const int n_it = (int)((bhi - blo + STEP - 1) / STEP);
+  uint4 r[U], rn[U];
+  auto load = [&](uint4 (&w)[U], int it) {
+    const int64_t base = blo + (int64_t)it * STEP;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int64_t v0 = base + (int64_t)(k * kTopThreads + tid) * VEC;
-      r[k] = load_stream(reinterpret_cast<const uint4 *>(row + (v0 < bhi ? v0 : blo)));
+      w[k] = load_stream(reinterpret_cast<const uint4 *>(row + (v0 < bhi ? v0 : blo)));
     }
+  };
+  if (n_it > 0) load(rn, 0);
+  for (int it = 0; it < n_it; ++it) {
+    const int64_t base = blo + (int64_t)it * STEP;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const bool ok = base + (int64_t)(k * kTopThreads + tid) * VEC < bhi;
+    for (int k = 0; k < U; ++k) r[k] = rn[k];
+    if (it + 1 < n_it) load(rn, it + 1);
+    float x[CH];
+    if (base + STEP <= bhi) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[k * VEC + e] = ok ? E::at(r[k], e) : -kInf;
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[k * VEC + e] = E::at(r[k], e);
+    } else {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool ok = base + (int64_t)(k * kTopThreads + tid) * VEC < bhi;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[k * VEC + e] = ok ? E::at(r[k], e) : -kInf;
+      }
     }
     // suppressed ids of this iteration (rare, workgroup-uniform)
     while (sp < a.n_suppress && a.suppress[sp] < base) ++sp;
@@ -336,22 +379,33 @@ __global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
             if (k == ks && e == es) x[k * VEC + e] = -kInf;
       }
     }
-    auto idx_of = [&](int k, int j, int ln) -> int {
+    chunk_update<U, VEC, false, false>(st, x, [&](int k, int j, int ln) -> int {
       return (int)(base + (int64_t)(k * kTopThreads + wave * 64 + ln) * VEC + j);
-    };
-    chunk_update<U, VEC, false, false>(st, x, idx_of);
-    if (K > 0) top_update<U, VEC, true>(tl, K, x, idx_of);
+    });
+    if constexpr (TOP) {
+      float cm = x[0];
+#pragma unroll
+      for (int e = 1; e < CH; ++e) cm = fmaxf(cm, x[e]);
+      tmax = fmaxf(tmax, cm);
+      const bool renew = it < 8 && (it & (it + 1)) == 0;
+      if (renew) bound = group_bound(tmax, K, gm[__builtin_popcount(it) & 1]);
+      const float least = least_candidate(bound, renew);
+      if (__builtin_amdgcn_ballot_w64(cm >= least) != 0)
+        collect<U, VEC>(tc, K, x, least, [&](int k, int j) -> int {
+          return (int)(base + (int64_t)(k * kTopThreads + tid) * VEC + j);
+        });
+    }
   }
   const int nh = (int)(blo - lo), nq = (int)(hi - bhi);
   if (wave == 0 && nh + nq > 0) {
     float x1[1] = {-kInf};
     const int64_t v = lane < nh ? lo + lane : bhi + (lane - nh);
     if (lane < nh + nq && !suppressed(a, v)) x1[0] = E::load1(row + v);
-    auto idx_of = [&](int, int, int ln) -> int {
+    chunk_update<1, 1, true, false>(st, x1, [&](int, int, int ln) -> int {
       return (int)(ln < nh ? lo + ln : bhi + (ln - nh));
-    };
-    chunk_update<1, 1, true, false>(st, x1, idx_of);
-    if (K > 0) top_update<1, 1, false>(tl, K, x1, idx_of);
+    });
+    if constexpr (TOP)
+      collect<1, 1>(tc, K, x1, least_candidate(bound, true), [&](int, int) -> int { return (int)v; });
   }
 
   // wave partials -> the workgroup's
@@ -362,15 +416,22 @@ __global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
   p.S = wave_sum(st.S) + st.Sx;
   to_max_relative(st, p.z, p.S);
   if (lane == 0) wave_parts[wave] = p;
-  if (lane < K) keys[wave * K + lane] = top_key(tl.v, tl.id);
   __syncthreads();
   if (wave == 0) {
     const Partial q =
         butterfly_merge<false>(lane < kTopWaves ? wave_parts[lane] : empty_partial(), kTopWaves, a.c);
     if (lane == 0) s_part = q;
   }
-  if (K > 0) select_keys(keys, kTopWaves * K, K, cand, &s_ncand, &s_bound, best);
-  else __syncthreads();
+  if constexpr (TOP) {
+    uint64_t mine[kCap / 64];
+#pragma unroll
+    for (int j = 0; j < kCap / 64; ++j) mine[j] = lane + 64 * j < tc.n ? tc.buf[lane + 64 * j] : kNoKey;
+    select_keys(mine, K, gm[0], cand, &s_ncand, best);
+  } else {
+    __syncthreads();
+    if (K > 0 && tid == 0) best[0] = s_part.idx == kIdxNone ? kNoKey : top_key(s_part.M, s_part.idx);
+    __syncthreads();
+  }
 
   if (a.slices > 1) {
     // publish this slice; the row's last slice merges them in slice order
@@ -403,12 +464,18 @@ __global__ __launch_bounds__(kTopThreads) void logprob_kernel(LogprobArgs a) {
       q = butterfly_merge<false>(q, 64, a.c);
       if (lane == 0) s_part = q;
     }
-    if (K > 0) {
-      for (int i = tid; i < a.slices * K; i += kTopThreads)
-        keys[i] = load_coh(&all[(int64_t)(i / K) * words + 2 + i % K]);
-      __syncthreads();
-      select_keys(keys, a.slices * K, K, cand, &s_ncand, &s_bound, best);
+    if constexpr (TOP) {
+      constexpr int N = kKeys / kTopThreads;
+      uint64_t mine[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = tid + j * kTopThreads;
+        mine[j] = i < a.slices * K ? load_coh(&all[(int64_t)(i / K) * words + 2 + i % K]) : kNoKey;
+      }
+      select_keys(mine, K, gm[1], cand, &s_ncand, best);
     } else {
+      __syncthreads();
+      if (K > 0 && tid == 0) best[0] = s_part.idx == kIdxNone ? kNoKey : top_key(s_part.M, s_part.idx);
       __syncthreads();
     }
     // leave the workspace zeroed
@@ -648,10 +715,15 @@ extern "C" int dllm_token_logprobs(const void *logits, int dtype, int64_t B, int
                                            align256((size_t)rows * 4));
   }
   const dim3 grid((uint32_t)(rows * p.slices));
-  if (dtype == DLLM_BF16)
-    hipLaunchKernelGGL(logprob_kernel<uint16_t>, grid, dim3(kTopThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL(logprob_kernel<float>, grid, dim3(kTopThreads), 0, stream, a);
+  // one alternative is the maximum that the statistics keep anyway
+  const dim3 block(kTopThreads);
+  if (dtype == DLLM_BF16) {
+    if (top > 1) hipLaunchKernelGGL((logprob_kernel<uint16_t, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((logprob_kernel<uint16_t, false>), grid, block, 0, stream, a);
+  } else {
+    if (top > 1) hipLaunchKernelGGL((logprob_kernel<float, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((logprob_kernel<float, false>), grid, block, 0, stream, a);
+  }
   return check_launch(who);
 }
 
