@@ -654,36 +654,61 @@ class StableConfidentStopping:
 
 
 # ---------------------------------------------------------------- scores of given tokens
+# A call of these has a microsecond or two of device work at its smallest, so
+# each argument is looked at once and named only when it is wrong.
 
-def _same(t, name, dtypes, shape, device):
-    """A contiguous tensor of this shape on the call's device."""
-    _bl(t, name, dtypes, torch.Size(shape))
+def _same(t, name, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape on the call's device."""
+    if isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and \
+            t.shape == shape and t.is_contiguous():
+        return t
+    _dev(t, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+    _bl(t, name, (dtype,), torch.Size(shape))
     return t
+
+
+def _launch(device, what, fn, *args):
+    """fn(*args, the device's current stream), with that device current."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status < 0:
+        _check(status, what)
 
 
 def _logits_args(logits):
     _dev(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits must be (B, L, V)")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    if logits.dtype is torch.bfloat16:
+        dt = DLLM_BF16
+    elif logits.dtype is torch.float32:
+        dt = DLLM_F32
+    else:
         raise ValueError("logits must be float32 or bfloat16")
-    return DLLM_BF16 if logits.dtype == torch.bfloat16 else DLLM_F32, _row_stride(logits)
+    return dt, logits.shape[2] if logits.is_contiguous() else _row_stride(logits)
 
 
 def _suppress_array(suppress_ids):
-    return (ctypes.c_int32 * max(len(suppress_ids), 1))(*[int(s) for s in suppress_ids])
+    if not len(suppress_ids):
+        return None
+    return (ctypes.c_int32 * len(suppress_ids))(*[int(s) for s in suppress_ids])
 
 
 _lp_sizes = {}
 
 
-def _logprobs_workspace(dev, stream, dt, B, L, V, top):
+def _logprobs_workspace(dev, dt, B, L, V, top):
     key = (dt, B, L, V, top, dev.index)
     need = _lp_sizes.get(key)
     if need is None:
-        need = int(load_library().dllm_token_logprobs_workspace_size(dt, B, L, V, top))
+        with _on(dev):
+            need = int(load_library().dllm_token_logprobs_workspace_size(dt, B, L, V, top))
         _lp_sizes[key] = need
     if need == 0:
         return None
@@ -691,34 +716,52 @@ def _logprobs_workspace(dev, stream, dt, B, L, V, top):
         # a buffer of the graph's own, cleared by a node of the graph, so that
         # graphs captured on one stream and replayed side by side share nothing
         return torch.zeros(need, dtype=torch.uint8, device=dev)
-    return _workspace(dev, stream, need)
+    return _workspace(dev, torch._C._cuda_getCurrentRawStream(dev.index), need)
 
 
 def _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace):
     dt, row_stride = _logits_args(logits)
     B, L, V = logits.shape
     dev = logits.device
-    _same(targets, "targets", (torch.int32,), (B, L), dev)
+    _same(targets, "targets", torch.int32, (B, L), dev)
     top = int(top)
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top must be in [0, {MAX_TOP}]")
-    sup = _suppress_array(suppress_ids)
     logprob = torch.empty((B, L), dtype=torch.float32, device=dev)
     entropy = torch.empty((B, L), dtype=torch.float32, device=dev)
     norm = torch.empty((B, L, 2), dtype=torch.float32, device=dev)
-    ids = torch.empty((B, L, top), dtype=torch.int32, device=dev) if top else None
-    lps = torch.empty((B, L, top), dtype=torch.float32, device=dev) if top else None
-    with _on(dev):
-        stream = _stream(logits)
-        if workspace is None:
-            workspace = _logprobs_workspace(dev, stream, dt, B, L, V, top)
-        _check(load_library().dllm_token_logprobs(
-            logits.data_ptr(), dt, B, L, V, row_stride, float(temperature), sup,
+    ids = lps = ids_p = lps_p = ws_p = None
+    ws_n = 0
+    if top:
+        ids = torch.empty((B, L, top), dtype=torch.int32, device=dev)
+        lps = torch.empty((B, L, top), dtype=torch.float32, device=dev)
+        ids_p, lps_p = ids.data_ptr(), lps.data_ptr()
+    if workspace is None:
+        workspace = _logprobs_workspace(dev, dt, B, L, V, top)
+    else:
+        _bl(workspace, "workspace", (torch.uint8,))
+        if workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+    if workspace is not None:
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel()
+    _launch(dev, "dllm_token_logprobs", load_library().dllm_token_logprobs, logits.data_ptr(), dt,
+            B, L, V, row_stride, float(temperature), _suppress_array(suppress_ids),
             len(suppress_ids), targets.data_ptr(), top, logprob.data_ptr(), entropy.data_ptr(),
-            norm.data_ptr(), ids.data_ptr() if top else None, lps.data_ptr() if top else None,
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() if workspace is not None else 0, stream), "dllm_token_logprobs")
+            norm.data_ptr(), ids_p, lps_p, ws_p, ws_n)
     return Logprobs(logprob, entropy, ids, lps, norm)
+
+
+def _grad_call(logits, targets, norm, entropy, g_logprob, g_entropy, temperature, suppress_ids,
+               out):
+    dt, row_stride = _logits_args(logits)
+    B, L, V = logits.shape
+    _launch(logits.device, "dllm_token_logprobs_grad", load_library().dllm_token_logprobs_grad,
+            logits.data_ptr(), dt, B, L, V, row_stride, float(temperature),
+            _suppress_array(suppress_ids), len(suppress_ids), targets.data_ptr(), norm.data_ptr(),
+            entropy.data_ptr(), g_logprob.data_ptr() if g_logprob is not None else None,
+            g_entropy.data_ptr() if g_entropy is not None else None, out.data_ptr(),
+            V if out.is_contiguous() else _row_stride(out))
+    return out
 
 
 class _LogprobsFunction(torch.autograd.Function):
@@ -726,8 +769,11 @@ class _LogprobsFunction(torch.autograd.Function):
     def forward(ctx, logits, targets, temperature, suppress_ids, top, workspace):
         r = _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace)
         ctx.save_for_backward(logits, targets, r.norm, r.entropy)
-        ctx.temperature, ctx.suppress_ids = temperature, suppress_ids
-        ctx.mark_non_differentiable(*(t for t in r[2:] if t is not None))
+        ctx.temperature, ctx.suppress_ids = temperature, tuple(suppress_ids)
+        if top:
+            ctx.mark_non_differentiable(r.norm, r.top_ids, r.top_logprobs)
+        else:
+            ctx.mark_non_differentiable(r.norm)
         ctx.set_materialize_grads(False)
         return tuple(r)
 
@@ -737,12 +783,12 @@ class _LogprobsFunction(torch.autograd.Function):
         if g_logprob is None and g_entropy is None:
             return (None,) * 6
         logits, targets, norm, entropy = ctx.saved_tensors
-        grad = token_logprobs_grad(
-            logits, targets, norm, entropy,
-            None if g_logprob is None else g_logprob.contiguous(),
-            None if g_entropy is None else g_entropy.contiguous(),
-            temperature=ctx.temperature, suppress_ids=ctx.suppress_ids)
-        return (grad,) + (None,) * 5
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _grad_call(logits, targets, norm, entropy,
+                   None if g_logprob is None else g_logprob.contiguous(),
+                   None if g_entropy is None else g_entropy.contiguous(), ctx.temperature,
+                   ctx.suppress_ids, grad)
+        return grad, None, None, None, None, None
 
 
 def token_logprobs(logits, targets, temperature=1.0, suppress_ids=(), top=0, workspace=None):
@@ -769,28 +815,22 @@ def token_logprobs_grad(logits, targets, norm, entropy, grad_logprob, grad_entro
     """Gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with
     respect to the logits, from token_logprobs' norm and entropy.  Either
     gradient may be None.  ``out`` may be the logits themselves."""
-    dt, row_stride = _logits_args(logits)
+    _logits_args(logits)
     B, L, V = logits.shape
     dev = logits.device
-    _same(targets, "targets", (torch.int32,), (B, L), dev)
-    _same(norm, "norm", (torch.float32,), (B, L, 2), dev)
-    _same(entropy, "entropy", (torch.float32,), (B, L), dev)
+    _same(targets, "targets", torch.int32, (B, L), dev)
+    _same(norm, "norm", torch.float32, (B, L, 2), dev)
+    _same(entropy, "entropy", torch.float32, (B, L), dev)
     for g, name in ((grad_logprob, "grad_logprob"), (grad_entropy, "grad_entropy")):
         if g is not None:
-            _same(g, name, (torch.float32,), (B, L), dev)
+            _same(g, name, torch.float32, (B, L), dev)
     if out is None:
         out = torch.empty((B, L, V), dtype=logits.dtype, device=dev)
     _dev(out, "out")
     if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
         raise ValueError("out must have the logits' dtype, shape and device")
-    with _on(dev):
-        _check(load_library().dllm_token_logprobs_grad(
-            logits.data_ptr(), dt, B, L, V, row_stride, float(temperature),
-            _suppress_array(suppress_ids), len(suppress_ids), targets.data_ptr(), norm.data_ptr(),
-            entropy.data_ptr(), grad_logprob.data_ptr() if grad_logprob is not None else None,
-            grad_entropy.data_ptr() if grad_entropy is not None else None, out.data_ptr(),
-            _row_stride(out), _stream(logits)), "dllm_token_logprobs_grad")
-    return out
+    return _grad_call(logits, targets, norm, entropy, grad_logprob, grad_entropy, temperature,
+                      suppress_ids, out)
 
 
 # ---------------------------------------------------------------- the 8-bit key/value cache
@@ -821,36 +861,45 @@ class KVCache:
 def _cache(cache):
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
-    return _dev(cache.k, "cache"), ctypes.byref(cache._c)
+    if cache.device.type != "cuda":
+        _dev(cache.k, "cache")
+    return cache.device, ctypes.byref(cache._c)
 
 
 def _table(t, name, B, device):
     """A (B, pages) int32 page table, rows of unit stride (a slice of a larger
     table will do); returns (pages, row stride)."""
     _dev(t, name)
-    if t.dtype != torch.int32 or t.dim() != 2 or t.device != device:
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.device != device:
         raise ValueError(f"{name} must be a (B, pages) int32 tensor on {device}")
-    if B is not None and t.shape[0] != B:
-        raise ValueError(f"{name} has {t.shape[0]} rows, not {B}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, pages = t.shape
+    if B is not None and rows != B:
+        raise ValueError(f"{name} has {rows} rows, not {B}")
+    if t.is_contiguous():
+        return pages, pages
+    if pages > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} rows must have unit stride")
-    return t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return pages, t.stride(0) if rows > 1 else pages
+
+
+_Strides = ctypes.c_int64 * 3
 
 
 def _heads(t, name, shape, device):
     """A (B, L, heads, head_dim) bfloat16 tensor with unit stride along the last
     dimension; returns its element strides as a C array."""
     _dev(t, name)
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.device != device:
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be a {tuple(shape)} bfloat16 tensor on {device}, not "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.numel() and t.stride(3) != 1:
+    st = t.stride()
+    if st[3] != 1 and t.numel():
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+    return _Strides(st[0], st[1], st[2])
 
 
 def _ints(t, name, B, device):
-    return None if t is None else _same(t, name, (torch.int32,), (B,), device).data_ptr()
+    return None if t is None else _same(t, name, torch.int32, (B,), device).data_ptr()
 
 
 def kv_write(cache, k, v, page_table, start, lens=None):
@@ -858,39 +907,35 @@ def kv_write(cache, k, v, page_table, start, lens=None):
     start[b] + lens[b] - 1 (lens None: L) of every sequence, whose pages
     page_table (B, pages) names; the sequence then ends there.  Tokens before
     start[b] stay.  start, lens: (B,) int32."""
-    pool, c = _cache(cache)
-    dev = pool.device
+    dev, c = _cache(cache)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be (B, L, kv_heads, head_dim)")
     B, L = k.shape[:2]
-    ks = _heads(k, "k", (B, L, cache.kv_heads, cache.head_dim), dev)
-    vs = _heads(v, "v", (B, L, cache.kv_heads, cache.head_dim), dev)
+    shape = (B, L, cache.kv_heads, cache.head_dim)
+    ks = _heads(k, "k", shape, dev)
+    vs = _heads(v, "v", shape, dev)
     pages, stride = _table(page_table, "page_table", B, dev)
     s = _ints(start, "start", B, dev)
     if s is None:
         raise ValueError("start must be given")
-    with _on(dev):
-        _check(load_library().dllm_kv_write(c, k.data_ptr(), ks, v.data_ptr(), vs, B, L,
-                                            page_table.data_ptr(), pages, stride, s,
-                                            _ints(lens, "lens", B, dev), _stream(pool)),
-               "dllm_kv_write")
+    _launch(dev, "dllm_kv_write", load_library().dllm_kv_write, c, k.data_ptr(), ks, v.data_ptr(),
+            vs, B, L, page_table.data_ptr(), pages, stride, s, _ints(lens, "lens", B, dev))
 
 
 def kv_read(cache, page_table, lens):
     """(k, v), each (B, KV_PAGE * pages, kv_heads, head_dim) bfloat16: the values
     the cache stands for, 0 past lens[b]."""
-    pool, c = _cache(cache)
-    dev = pool.device
+    dev, c = _cache(cache)
     pages, stride = _table(page_table, "page_table", None, dev)
     B = page_table.shape[0]
     n = _ints(lens, "lens", B, dev)
-    k = torch.empty((B, pages * KV_PAGE, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16,
-                    device=dev)
-    v = torch.empty_like(k)
-    with _on(dev):
-        _check(load_library().dllm_kv_read(c, B, page_table.data_ptr(), pages, stride, n,
-                                           k.data_ptr(), v.data_ptr(), _stream(pool)),
-               "dllm_kv_read")
+    if n is None:
+        raise ValueError("lens must be given")
+    shape = (B, pages * KV_PAGE, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _launch(dev, "dllm_kv_read", load_library().dllm_kv_read, c, B, page_table.data_ptr(), pages,
+            stride, n, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -903,8 +948,9 @@ def _attn_size(B, L, Hq, H, D, pages, device):
     need = _attn_sizes.get(key)
     if need is None:
         lib = load_library()
-        need = (int(lib.dllm_block_attention_workspace_size(B, L, Hq, H, D, pages)),
-                int(lib.dllm_attention_weights_workspace_size(B, L, Hq, H, pages)))
+        with _on(device):
+            need = (int(lib.dllm_block_attention_workspace_size(B, L, Hq, H, D, pages)),
+                    int(lib.dllm_attention_weights_workspace_size(B, L, Hq, H, pages)))
         _attn_sizes[key] = need
     return need
 
@@ -923,46 +969,45 @@ def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, bl
     ``weights`` (B, KV_PAGE * pages) float32: every cached token's attention
     weight, summed over queries and heads, is added to it (see kv_evict).
     """
-    pool, c = _cache(cache)
-    dev = pool.device
+    dev, c = _cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be (B, L, q_heads, head_dim)")
     B, L, Hq, D = q.shape
-    qs = _heads(q, "q", (B, L, Hq, cache.head_dim), dev)
+    shape = (B, L, Hq, cache.head_dim)
+    qs = _heads(q, "q", shape, dev)
     pages, stride = _table(page_table, "page_table", B, dev)
     n = _ints(kv_lens, "kv_lens", B, dev)
     if n is None:
         raise ValueError("kv_lens must be given")
     qstart, qlens = _ints(q_start, "q_start", B, dev), _ints(q_lens, "q_lens", B, dev)
     if out is None:
-        out = (torch.empty if q_lens is None else torch.zeros)((B, L, Hq, D), dtype=torch.bfloat16,
+        out = (torch.empty if q_lens is None else torch.zeros)(shape, dtype=torch.bfloat16,
                                                                 device=dev)
-    os_ = _heads(out, "out", (B, L, Hq, D), dev)
+    os_ = _heads(out, "out", shape, dev)
     if lse is None:
         lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
         if q_lens is not None:
             lse.fill_(-math.inf)
-    _same(lse, "lse", (torch.float32,), (B, Hq, L), dev)
+    else:
+        _same(lse, "lse", torch.float32, (B, Hq, L), dev)
     if weights is not None:
-        _same(weights, "weights", (torch.float32,), (B, pages * KV_PAGE), dev)
+        _same(weights, "weights", torch.float32, (B, pages * KV_PAGE), dev)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    need, need_w = _attn_size(B, L, Hq, cache.kv_heads, D, pages, dev)
+    if weights is not None:
+        need = max(need, need_w)
+    # any content will do: a block of torch's allocator per call, so that neither
+    # streams nor captured graphs share one
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws_p = ws.data_ptr() if need else None
     lib = load_library()
-    with _on(dev):
-        need, need_w = _attn_size(B, L, Hq, cache.kv_heads, D, pages, dev)
-        if weights is not None:
-            need = max(need, need_w)
-        # any content will do: a block of torch's allocator per call, so that
-        # neither streams nor captured graphs share one
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        ws_p = ws.data_ptr() if need else None
-        stream = _stream(pool)
-        head = (c, q.data_ptr(), qs, B, L, Hq, page_table.data_ptr(), pages, stride, n, qstart,
-                qlens, int(block_len), scale)
-        _check(lib.dllm_block_attention(*head, out.data_ptr(), os_, lse.data_ptr(), ws_p, need,
-                                        stream), "dllm_block_attention")
-        if weights is not None:
-            _check(lib.dllm_attention_weights(*head, lse.data_ptr(), weights.data_ptr(), ws_p, need,
-                                              stream), "dllm_attention_weights")
+    args = (c, q.data_ptr(), qs, B, L, Hq, page_table.data_ptr(), pages, stride, n, qstart, qlens,
+            int(block_len), scale)
+    _launch(dev, "dllm_block_attention", lib.dllm_block_attention, *args, out.data_ptr(), os_,
+            lse.data_ptr(), ws_p, need)
+    if weights is not None:
+        _launch(dev, "dllm_attention_weights", lib.dllm_attention_weights, *args, lse.data_ptr(),
+                weights.data_ptr(), ws_p, need)
     return Attention(out, lse)
 
 
@@ -974,7 +1019,7 @@ def evict_select(weights, kv_lens, budget, sink=0, recent=0, new_T=None):
     increasing, -1 behind the last; lens (B,) int32; their weights (B, new_T),
     0 behind the last)."""
     _dev(weights, "weights")
-    if weights.dtype != torch.float32 or weights.dim() != 2 or \
+    if weights.dtype is not torch.float32 or weights.dim() != 2 or \
             (weights.shape[1] > 1 and weights.stride(1) != 1):
         raise ValueError("weights must be a (B, T) float32 tensor with rows of unit stride")
     B, T = weights.shape
@@ -987,11 +1032,9 @@ def evict_select(weights, kv_lens, budget, sink=0, recent=0, new_T=None):
     kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
     lens = torch.empty((B,), dtype=torch.int32, device=dev)
     new_w = torch.empty((B, new_T), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(load_library().dllm_evict_select(
-            weights.data_ptr(), B, T, weights.stride(0) if B > 1 else T, n, budget, int(sink),
-            int(recent), kept.data_ptr(), lens.data_ptr(), new_w.data_ptr(), new_T,
-            _stream(weights)), "dllm_evict_select")
+    _launch(dev, "dllm_evict_select", load_library().dllm_evict_select, weights.data_ptr(), B, T,
+            weights.stride(0) if B > 1 else T, n, budget, int(sink), int(recent), kept.data_ptr(),
+            lens.data_ptr(), new_w.data_ptr(), new_T)
     return Evicted(kept, lens, new_w)
 
 
@@ -999,19 +1042,16 @@ def kv_gather(cache, page_table, kept, counts, new_pages):
     """Token j < counts[b] on the pages of new_pages (B, pages) becomes token
     kept[b, j] of the sequence on page_table.  kept increases along its rows; no
     page of new_pages may be in use."""
-    pool, c = _cache(cache)
-    dev = pool.device
+    dev, c = _cache(cache)
     pages, stride = _table(page_table, "page_table", None, dev)
     B = page_table.shape[0]
     npages, nstride = _table(new_pages, "new_pages", B, dev)
     if not isinstance(kept, torch.Tensor) or kept.dim() != 2:
         raise ValueError("kept must be (B, n)")
-    _same(kept, "kept", (torch.int32,), (B, kept.shape[1]), dev)
-    counts_p = _ints(counts, "counts", B, dev)
-    with _on(dev):
-        _check(load_library().dllm_kv_gather(
-            c, B, page_table.data_ptr(), pages, stride, kept.data_ptr(), kept.shape[1], counts_p,
-            new_pages.data_ptr(), npages, nstride, _stream(pool)), "dllm_kv_gather")
+    _same(kept, "kept", torch.int32, (B, kept.shape[1]), dev)
+    _launch(dev, "dllm_kv_gather", load_library().dllm_kv_gather, c, B, page_table.data_ptr(),
+            pages, stride, kept.data_ptr(), kept.shape[1], _ints(counts, "counts", B, dev),
+            new_pages.data_ptr(), npages, nstride)
 
 
 def kv_evict(cache, page_table, kv_lens, weights, budget, new_pages, sink=0, recent=0):
@@ -1021,13 +1061,15 @@ def kv_evict(cache, page_table, kv_lens, weights, budget, new_pages, sink=0, rec
     pages are then free.  Returns Evicted: the kept positions, the new lengths,
     and the kept tokens' weights (B, KV_PAGE * new_pages.shape[1]), which go on
     accumulating."""
-    pool, _ = _cache(cache)
-    pages, _ = _table(page_table, "page_table", None, pool.device)
-    npages, _ = _table(new_pages, "new_pages", page_table.shape[0], pool.device)
+    dev, _ = _cache(cache)
+    pages, _ = _table(page_table, "page_table", None, dev)
+    B = page_table.shape[0]
+    npages, _ = _table(new_pages, "new_pages", B, dev)
     if npages * KV_PAGE < int(budget):
         raise ValueError("new_pages cannot hold budget tokens")
-    _same(weights, "weights", (torch.float32,), (page_table.shape[0], pages * KV_PAGE),
-          pool.device)
+    if new_pages.data_ptr() == page_table.data_ptr() and pages:
+        raise ValueError("new_pages is the page table")
+    _same(weights, "weights", torch.float32, (B, pages * KV_PAGE), dev)
     r = evict_select(weights, kv_lens, budget, sink, recent, new_T=npages * KV_PAGE)
     kv_gather(cache, page_table, r.kept, r.lens, new_pages)
     return r
