@@ -1,12 +1,12 @@
 // dllm_evict_select: the tokens of each cache that an eviction keeps.
 //
-// One workgroup per sequence.  The weights' order-preserving keys (best first,
-// common.h; a protected token's key is 0, before every weight's) are selected
-// by radix: three histograms of 11, 11 and 10 bits find the budget-th smallest
-// key, then two sweeps place the kept positions in order, each wave its own
-// run of the sequence, with one prefix over the waves between them.  The
-// weights are read from HBM once and from L2 afterwards; the work is bound by
-// the sweeps' latency in one workgroup.
+// One workgroup per sequence, each wave a run of it.  The weights' order-
+// preserving keys (best first, common.h; a protected token's key is 0, before
+// every weight's) are read once, into registers up to 32768 tokens.  Three
+// histograms of 11, 11 and 10 bits find the budget-th smallest key; then each
+// wave counts and places its kept positions in order, with one prefix over the
+// waves between.  One workgroup's latency bounds it: about 14 us for 32768
+// tokens, where sweeps that read the weights again each time took 59 us.
 #include <algorithm>
 
 #include "common.h"
@@ -25,11 +25,15 @@ struct SelectArgs {
   float *new_weights;
 };
 
+// R keys per thread in registers (n <= R * 1024), or, with R = 0, read again in
+// every sweep.
+template <int R>
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a) {
   __shared__ uint32_t hist[2048];
   __shared__ uint32_t s_digit, s_below;
-  __shared__ int s_wave[kSelThreads / 64], s_less[kSelWaves], s_same[kSelWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int s_wave[kSelWaves], s_less[kSelWaves], s_same[kSelWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t b = blockIdx.x;
   const float *w = a.weights + b * a.weights_stride;
   const int n = (int)(a.lens[b] < 0 ? 0 : min((int64_t)a.lens[b], a.T));
@@ -47,9 +51,46 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
     }
     return;
   }
+  // this wave's tokens: 64 i + lane of [lo, hi)
   const int sink = (int)a.sink, tail = n - (int)a.recent;
-  auto key_of = [&](int t) -> uint32_t {
-    return t < sink || t >= tail ? 0u : conf_key(w[t]);
+  const int run = ((n + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
+  const int lo = min(wave * run, n), hi = min(lo + run, n);
+  auto key_at = [&](int t, float x) -> uint32_t { return t < sink || t >= tail ? 0u : conf_key(x); };
+  uint32_t key[R > 0 ? R : 1];                // ~0 past the end
+  if constexpr (R > 0) {
+    float x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {              // every load in flight before the first is used
+      const int t = lo + 64 * i + lane;
+      x[i] = w[t < hi ? t : 0];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = lo + 64 * i + lane;
+      key[i] = t < hi ? key_at(t, x[i]) : ~0u;
+    }
+  }
+  // calls f(first token, key) for every 64 of the wave's tokens
+  auto sweep = [&](auto f) {
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (lo + 64 * i < hi) f(lo + 64 * i, key[i]);
+    } else {
+      for (int t0 = lo; t0 < hi; t0 += 64 * 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = t0 + 64 * i + lane;
+          x[i] = w[t < hi ? t : 0];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = t0 + 64 * i + lane;
+          if (t0 + 64 * i < hi) f(t0 + 64 * i, t < hi ? key_at(t, x[i]) : ~0u);
+        }
+      }
+    }
   };
 
   // the keep-th smallest key: digit by digit from the top
@@ -61,10 +102,19 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
     const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
     for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int t = tid; t < n; t += kSelThreads) {
-      const uint32_t k = key_of(t);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1u);
-    }
+    sweep([&](int t0, uint32_t k) {
+      const bool in = t0 + lane < hi && (k & mask) == prefix;
+      const uint32_t bin = (k >> shift) & bits;
+      // one count for a wave of one bin (equal weights would queue for it)
+      const uint64_t m = __builtin_amdgcn_ballot_w64(in);
+      if (m == 0) return;
+      const int first = __builtin_amdgcn_readlane((int)bin, __builtin_ctzll(m));
+      if (__builtin_amdgcn_ballot_w64(in && bin != (uint32_t)first) == 0) {
+        if (lane == 0) atomicAdd(&hist[first], (uint32_t)__builtin_popcountll(m));
+      } else if (in) {
+        atomicAdd(&hist[bin], 1u);
+      }
+    });
     __syncthreads();
     // inclusive prefix over the bins, two per thread; the digit's bin is the
     // first whose prefix reaches want
@@ -93,35 +143,41 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
   }
 
   // keys below the threshold all stay, and the first `want` equal to it
-  const int run = ((n + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
-  const int lo = min(wave * run, n), hi = min(lo + run, n);
   int less = 0, same = 0;
-  for (int t0 = lo; t0 < hi; t0 += 64) {
-    const int t = t0 + lane;
-    const uint32_t k = t < hi ? key_of(t) : ~0u;
-    less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t < hi && k < prefix));
-    same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t < hi && k == prefix));
-  }
+  sweep([&](int t0, uint32_t k) {
+    less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t0 + lane < hi && k < prefix));
+    same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t0 + lane < hi && k == prefix));
+  });
   if (lane == 0) { s_less[wave] = less; s_same[wave] = same; }
   __syncthreads();
   int at_less = 0, at_same = 0;
   for (int i = 0; i < wave; ++i) { at_less += s_less[i]; at_same += s_same[i]; }
   const uint64_t below = (1ull << lane) - 1ull;
-  for (int t0 = lo; t0 < hi; t0 += 64) {
+  sweep([&](int t0, uint32_t k) {
     const int t = t0 + lane;
-    const uint32_t k = t < hi ? key_of(t) : ~0u;
     const bool is_less = t < hi && k < prefix, is_same = t < hi && k == prefix;
     const uint64_t ml = __builtin_amdgcn_ballot_w64(is_less);
     const uint64_t ms = __builtin_amdgcn_ballot_w64(is_same);
     const int rl = at_less + __builtin_popcountll(ml & below);
     const int rs = at_same + __builtin_popcountll(ms & below);
-    if (is_less || (is_same && rs < (int)want)) {
-      const int j = rl + min(rs, (int)want);
-      kept[j] = t;
-      if (nw) nw[j] = w[t];
-    }
+    if (is_less || (is_same && rs < (int)want)) kept[rl + min(rs, (int)want)] = t;
     at_less += __builtin_popcountll(ml);
     at_same += __builtin_popcountll(ms);
+  });
+  if (nw) {
+    // the kept tokens' weights, from the positions the workgroup has just stored
+    // (a load beside each store above would wait for memory 64 tokens at a time)
+    __syncthreads();
+    for (int j0 = 0; j0 < keep; j0 += 8 * kSelThreads) {
+      int t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = kept[min(j0 + i * kSelThreads + tid, keep - 1)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i * kSelThreads + tid;
+        if (j < keep) nw[j] = w[t[i]];
+      }
+    }
   }
 }
 
@@ -152,6 +208,11 @@ extern "C" int dllm_evict_select(const float *weights, int64_t B, int64_t T,
     return fail(DLLM_ERR_ARG, "%s: new_weights aliases weights", who);
   const SelectArgs a{weights, weights_stride, T, budget, sink, recent, new_T,
                      kv_lens, kept, new_lens, new_weights};
-  hipLaunchKernelGGL(evict_select_kernel, dim3((uint32_t)B), dim3(kSelThreads), 0, stream, a);
+  const dim3 grid((uint32_t)B), block(kSelThreads);
+  // keys per thread for the longest sequence there can be
+  if (T <= 4 * kSelThreads) hipLaunchKernelGGL(evict_select_kernel<4>, grid, block, 0, stream, a);
+  else if (T <= 32 * kSelThreads)
+    hipLaunchKernelGGL(evict_select_kernel<32>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(evict_select_kernel<0>, grid, block, 0, stream, a);
   return check_launch(who);
 }

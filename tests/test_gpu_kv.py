@@ -197,6 +197,17 @@ def test_evict_select_values(T):
             assert np.array_equal(r.lens.cpu().numpy(), nl)
 
 
+def test_evict_select_long():
+    """More tokens than one workgroup holds in registers, and all weights equal."""
+    rng = np.random.default_rng(1)
+    T = 70001
+    w = np.stack([np.exp(rng.normal(0, 3, T)), np.zeros(T)]).astype(np.float32)
+    for budget in (100, 50000):
+        r = dc.evict_select(torch.from_numpy(w).cuda(), _i32([T, T]), budget, 4, 64)
+        kept, nl = okv.evict_select(w, [T, T], budget, 4, 64)
+        assert np.array_equal(r.kept.cpu().numpy(), kept) and np.array_equal(r.lens.cpu().numpy(), nl)
+
+
 # ---------------------------------------------------------------- attention
 
 def _attention_case(seed, B, L, Hq, H, D, T, lens, table=None, scale_q=1.0):
@@ -319,6 +330,30 @@ def test_attention_large_scores_and_far_scales():
     q = _bf16(rng.normal(0, 0.1, (1, L, Hq, D)))
     _check_attention(cache, ref, table, q, [T], n)
     _check_attention(cache, ref, table, q, [32], n)               # the small page alone
+
+
+def test_a_large_page_that_nothing_attends_to_costs_no_bits():
+    """A page of values 2^50 times the others' whose weight is below 2^-90: the
+    others' values come out as exactly as without it."""
+    rng = np.random.default_rng(12)
+    T, D = 96, 64
+    table = np.array([[0, 1, 2]], dtype=np.int32)
+    k, v = rng.normal(0, 0.05, (1, T, 1, D)), rng.normal(0, 1, (1, T, 1, D))
+    k[0, 32:64] = -3.0
+    v[0, 32:64] *= 2.0 ** 50
+    v[0, 64:] *= 2.0 ** -30
+    q = _bf16(np.full((1, 3, 1, D), 4.0))
+    cache, ref = dc.KVCache(3, 1, D), okv.Cache(3, 1, D)
+    kt, vt = _bf16(k), _bf16(v)
+    dc.kv_write(cache, kt.cuda(), vt.cuda(), _i32(table), _i32([0]))
+    ref.write(_np(kt), _np(vt), table, [0])
+    r = dc.block_attention(q.cuda(), cache, _i32(table), _i32([T]))
+    rk, rv = ref.read(table, [T])
+    o, _, _, mass, _ = okv.block_attention(_np(q), rk, rv, table, [T], 3)
+    # the outputs are of order 1 though values of 2^50 are there; the tolerance
+    # has no term of their size
+    tol = 2.0 ** -8 * np.abs(o) + mass * (2.0 ** -11 + 2.0 ** -12)
+    assert (np.abs(_np(r.out) - o) <= tol).all() and np.abs(o).max() < 2
 
 
 def test_nan_query_stays_in_its_row():
