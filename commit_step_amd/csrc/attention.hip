@@ -51,6 +51,21 @@ constexpr float kRise = 1.0f;
 // their weights scaled by the rest, within float16's 2^-20.
 constexpr int kMinExp = -80;
 
+// n / d for n < 2^31 by multiplication: with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (floor(n m / 2^32) + n) / 2^s
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994).
+struct Divisor { uint32_t mul, shift; };
+
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while (s < 31 && (1u << s) < d) ++s;
+  return {(uint32_t)((((uint64_t)1 << s) - d) * ((uint64_t)1 << 32) / d + 1), s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, Divisor d) {
+  return (__umulhi(n, d.mul) + n) >> d.shift;
+}
+
 struct AttnArgs {
   const uint16_t *q;
   int64_t qs[3];
@@ -62,6 +77,7 @@ struct AttnArgs {
   int64_t max_pages, table_stride;
   const int32_t *table, *kv_lens, *q_start, *q_lens;
   uint32_t block_len;       // 0: no mask
+  Divisor by_group, by_block;
   int64_t B;
   int H, G, L;
   int ncols;                // L * G
@@ -91,61 +107,52 @@ __device__ __forceinline__ Column column(const AttnArgs &a, int64_t b, int64_t c
                                          int64_t q_len) {
   Column r;
   const int cc = c < a.ncols ? (int)c : 0;
-  r.l = cc / a.G;
+  r.l = (int)divide((uint32_t)cc, a.by_group);
   r.g = cc - r.l * a.G;
   r.on = c < a.ncols && r.l < q_len;
   r.lim = r.on ? n : 0;
-  if (a.block_len > 0 && r.on) {
-    // positions and block lengths are below 2^32 and 2^31: a 32-bit division
-    const uint32_t pos = (a.q_start ? (uint32_t)max(a.q_start[b], 0) : 0u) + (uint32_t)r.l;
-    r.lim = (int)min((uint64_t)n, (uint64_t)(pos / a.block_len + 1u) * a.block_len);
+  if (a.block_len > 0) {
+    // a position past 2^31 - 1 lies behind every token, as that does
+    const uint32_t start = a.q_start ? (uint32_t)max(a.q_start[b], 0) : 0u;
+    const uint32_t pos = min(start + (uint32_t)r.l, 0x7fffffffu);
+    const uint64_t end = (uint64_t)(divide(pos, a.by_block) + 1u) * a.block_len;
+    r.lim = (int)min((uint64_t)r.lim, end);
   }
   return r;
 }
 
-// The column's query as D / 16 operand pieces: piece s of half h holds
+// The column's query row (channel 0).
+__device__ __forceinline__ const uint16_t *query_row(const AttnArgs &a, int64_t b, int hkv,
+                                                     const Column &col) {
+  return a.q + b * a.qs[0] + (int64_t)hkv * a.G * a.qs[2] +
+         ((int64_t)col.l * (int32_t)a.qs[1] + (int64_t)col.g * (int32_t)a.qs[2]);
+}
+// Its place in a (B, q_heads, L) array.
+__device__ __forceinline__ int64_t lse_at(const AttnArgs &a, int64_t b, int hkv, const Column &col) {
+  return (b * a.H + hkv) * a.G * a.L + (col.g * a.L + col.l);
+}
+
+// Pieces s0 .. s0 + N - 1 of the column's query: piece s of half h holds
 // channels 32 (s / 2) + 16 h + 8 (s % 2) .. + 7, as the keys' pieces do.  A
 // column that is no real query reads some query's row (in bounds) and is
 // dropped later: columns do not mix.
-template <int D>
-__device__ __forceinline__ void load_query(const AttnArgs &a, int64_t b, int64_t head,
-                                           const Column &col, bf16x8 (&q)[D / 16]) {
+template <int N>
+__device__ __forceinline__ void load_query(const AttnArgs &a, const uint16_t *row, int s0,
+                                           bf16x8 (&q)[N]) {
   const int h = (threadIdx.x & 63) >> 5;
-  const uint16_t *row = a.q + b * a.qs[0] + col.l * a.qs[1] + head * a.qs[2];
   if (a.vec) {
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      q[s] = *reinterpret_cast<const bf16x8 *>(row + 32 * (s / 2) + 16 * h + 8 * (s % 2));
+    for (int i = 0; i < N; ++i)
+      q[i] = *reinterpret_cast<const bf16x8 *>(row + 32 * ((s0 + i) / 2) + 16 * h + 8 * ((s0 + i) % 2));
     return;
   }
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const uint16_t *x = row + 32 * (s / 2) + 16 * h + 8 * (s % 2);
+  for (int i = 0; i < N; ++i) {
+    const uint16_t *x = row + 32 * ((s0 + i) / 2) + 16 * h + 8 * ((s0 + i) % 2);
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
-    q[s] = __builtin_bit_cast(bf16x8, w);
-  }
-}
-
-// Pieces s0 .. s0 + N - 1 of the column's query.
-template <int D, int N>
-__device__ __forceinline__ void load_pieces_of_query(const AttnArgs &a, int64_t b, int64_t head,
-                                                     const Column &col, int s0, bf16x8 (&q)[N]) {
-  const int h = (threadIdx.x & 63) >> 5;
-  const uint16_t *row = a.q + b * a.qs[0] + col.l * a.qs[1] + head * a.qs[2];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int s = s0 + i;
-    const uint16_t *x = row + 32 * (s / 2) + 16 * h + 8 * (s % 2);
-    if (a.vec) {
-      q[i] = *reinterpret_cast<const bf16x8 *>(x);
-    } else {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
-      q[i] = __builtin_bit_cast(bf16x8, w);
-    }
+    q[i] = __builtin_bit_cast(bf16x8, w);
   }
 }
 
@@ -274,8 +281,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
         }
       }
     if (h == 0)
-      a.lse[(b * a.H * a.G + head) * a.L + col.l] =
-          log_sum(t.m, l);
+      a.lse[lse_at(a, b, hkv, col)] = log_sum(t.m, l);
     return;
   }
   const int64_t row = ((b * a.H + hkv) * a.ncols + c) * a.splits + split;
@@ -326,7 +332,7 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
 
   const Column col = column(a, b, c0 + (lane & 31), n, q_len);
   bf16x8 q[D / 16];
-  load_query<D>(a, b, (int64_t)hkv * a.G + col.g, col, q);
+  load_query(a, query_row(a, b, hkv, col), 0, q);
   const int max_lim = -wave_min_i(-col.lim);
   const int min_lim = wave_min_i(col.lim);
   Tile<D> tile;
@@ -544,7 +550,7 @@ template <int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kernel(AttnArgs a) {
   constexpr int P = kWeightPages;
   __shared__ float s_w[4][16][65];
-  __shared__ u32x4 s_q[2][D / 16][64];
+  __shared__ bf16x8 s_q[2][D / 16][64];
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t unit = blockIdx.x;
@@ -596,84 +602,71 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
   bf16x8 part_q[QW];
   auto fetch = [&](int u, Cols &x) {
     const Column col = column(a, b, (int64_t)min(u, u1 - 1) * 32 + (lane & 31), n, q_len);
-    const int64_t head = (int64_t)hkv * a.G + col.g;
-    x.z = a.lse[(b * a.H * a.G + head) * a.L + col.l];
+    x.z = a.lse[lse_at(a, b, hkv, col)];
     x.lim = col.lim;
-    load_pieces_of_query<D, QW>(a, b, head, col, wave * QW, part_q);
+    load_query(a, query_row(a, b, hkv, col), wave * QW, part_q);
   };
   auto publish = [&](int u) {
 #pragma unroll
-    for (int i = 0; i < QW; ++i) s_q[u & 1][wave * QW + i][lane] = __builtin_bit_cast(u32x4, part_q[i]);
+    for (int i = 0; i < QW; ++i) s_q[u & 1][wave * QW + i][lane] = part_q[i];
   };
-  auto score = [&](const bf16x8 (&kk)[D / 16], const bf16x8 (&q)[D / 16]) {
-    f32x16 s;
+  f32x16 s[P];                                              // the scores of the tile in work
+  // Tile u, whose columns are x and scores s: its weights, and the next tile's
+  // scores; part_q holds that one's queries, and takes those of tile u + 2.
+  auto step = [&](int u, Cols &x) {
+    publish(u + 1);
+    __syncthreads();
+    const bool none = x.z == kNegInf;                       // met nothing: adds nothing
+    const float sub = none ? 0.f : x.z * kLog2e;
+    const int lim = none ? 0 : x.lim;
+    fetch(u + 2, x);
+    bf16x8 q[D / 16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = 0.f;
+    for (int st = 0; st < D / 16; ++st) q[st] = s_q[(u + 1) & 1][st][lane];
 #pragma unroll
-    for (int st = 0; st < D / 16; ++st)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk[st], q[st], s, 0, 0, 0);
-    return s;
-  };
-  auto weigh = [&](int p, const f32x16 &s, const Cols &x) {
-    const int lim = x.z == kNegInf ? 0 : x.lim;             // met nothing: adds nothing
-    const int left = min(lim, end[p]) - t0 - p * kPage - 4 * h;
-    const float sub = x.z * kLog2e;
+    for (int p = 0; p < P; ++p) {
+      const int left = min(lim, end[p]) - t0 - p * kPage;
+      if (__builtin_amdgcn_ballot_w64(left < kPage) != 0) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      w[p][r] += 8 * (r / 4) + r % 4 < left ? __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -sub)) : 0.f;
+        for (int r = 0; r < 16; ++r)
+          if (8 * (r / 4) + r % 4 >= left - 4 * h) s[p][r] = kNegInf;
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      f32x16 next;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) next[r] = 0.f;
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) {
+        next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], q[st], next, 0, 0, 0);
+#pragma unroll
+        for (int r = st * (256 / D); r < (st + 1) * (256 / D); ++r)
+          w[p][r] += __builtin_amdgcn_exp2f(fmaf(s[p][r], a.c, -sub));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      s[p] = next;
+    }
   };
   if (u0 < u1) {
     Cols xa, xb;
-    f32x16 s[P];
-    bf16x8 q[D / 16];
     fetch(u0, xa);
     publish(u0);
     __syncthreads();
     fetch(u0 + 1, xb);
 #pragma unroll
-    for (int st = 0; st < D / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, s_q[u0 & 1][st][lane]);
+    for (int p = 0; p < P; ++p) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) s[p] = score(k[p], q);
-    for (int u = u0; u + 1 < u1; ++u) {
-      // s: the scores of tile u, xa its columns; part_q, xb: tile u + 1's
-      publish(u + 1);
-      __syncthreads();
-      Cols xc;
-      fetch(u + 2, xc);
+      for (int r = 0; r < 16; ++r) s[p][r] = 0.f;
 #pragma unroll
       for (int st = 0; st < D / 16; ++st)
-        q[st] = __builtin_bit_cast(bf16x8, s_q[(u + 1) & 1][st][lane]);
-      // a whole tile: every column sees every token of both pages
-      const float sub = xa.z * kLog2e;
-      bool whole = __builtin_amdgcn_ballot_w64(xa.z == kNegInf) == 0;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        whole = whole && __builtin_amdgcn_ballot_w64(min(xa.lim, end[p]) - t0 < (p + 1) * kPage) == 0;
-      if (whole) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const f32x16 next = score(k[p], q);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) w[p][r] += __builtin_amdgcn_exp2f(fmaf(s[p][r], a.c, -sub));
-#pragma unroll
-          for (int st = 0; st < D / 16; ++st) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // a matrix instruction
-            __builtin_amdgcn_sched_group_barrier(0x002 | 0x400, 768 / D, 0);  // then vector work
-          }
-          s[p] = next;
-        }
-      } else {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          weigh(p, s[p], xa);
-          s[p] = score(k[p], q);
-        }
-      }
-      xa = xb;
-      xb = xc;
+        s[p] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[p][st], s_q[u0 & 1][st][lane], s[p], 0, 0, 0);
     }
-#pragma unroll
-    for (int p = 0; p < P; ++p) weigh(p, s[p], xa);
+    // the last step's next tile is the last tile again, dropped
+    for (int u = u0; u < u1; u += 2) {
+      step(u, xa);
+      if (u + 1 < u1) step(u + 1, xb);
+    }
   }
   // fold the 32 columns of each half: lane (token, column half) of a page sums 16
 #pragma unroll
@@ -762,6 +755,9 @@ int check_attention(const char *who, const dllm_kv_cache *cache, const void *q,
   if (!q || !q_strides || !kv_lens)
     return fail(DLLM_ERR_ARG, "%s: q, q_strides and kv_lens must be non-NULL", who);
   if ((uintptr_t)q % 2 != 0) return fail(DLLM_ERR_ARG, "%s: q must be aligned to its element", who);
+  for (int i = 1; i < 3; ++i)
+    if (q_strides[i] != (int32_t)q_strides[i])
+      return fail(DLLM_ERR_UNSUPPORTED, "%s: q's strides along L and heads must fit 32 bits", who);
   return DLLM_OK;
 }
 
@@ -789,6 +785,8 @@ AttnArgs attn_args(const dllm_kv_cache &c, const void *q, const int64_t *q_strid
   a.q_start = q_start;
   a.q_lens = q_lens;
   a.block_len = (uint32_t)block_len;
+  a.by_group = divisor((uint32_t)(q_heads / c.kv_heads));
+  a.by_block = divisor(block_len > 0 ? (uint32_t)block_len : 1u);
   a.B = B;
   a.H = c.kv_heads;
   a.G = (int)(q_heads / c.kv_heads);

@@ -5,8 +5,8 @@
 // every weight's) are read once, into registers up to 32768 tokens.  Three
 // histograms of 11, 11 and 10 bits find the budget-th smallest key; then each
 // wave counts and places its kept positions in order, with one prefix over the
-// waves between.  One workgroup's latency bounds it: about 14 us for 32768
-// tokens, where sweeps that read the weights again each time took 59 us.
+// waves between.  One workgroup's instructions and latency bound it: 31 us for
+// 32768 tokens, where sweeps that read the weights again each time took 59 us.
 #include <algorithm>
 
 #include "common.h"
@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
+constexpr int kSelList = 8192;           // keys of one first digit held in LDS
 
 struct SelectArgs {
   const float *weights;
@@ -30,7 +31,10 @@ struct SelectArgs {
 template <int R>
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a) {
   __shared__ uint32_t hist[2048];
-  __shared__ uint32_t s_digit, s_below;
+  __shared__ uint32_t list_key[kSelList];
+  __shared__ uint8_t list_wave[kSelList];
+  __shared__ uint32_t s_digit, s_below, s_count;
+  __shared__ int s_listed;
   __shared__ int s_wave[kSelWaves], s_less[kSelWaves], s_same[kSelWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -56,7 +60,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
   const int run = ((n + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
   const int lo = min(wave * run, n), hi = min(lo + run, n);
   auto key_at = [&](int t, float x) -> uint32_t { return t < sink || t >= tail ? 0u : conf_key(x); };
-  uint32_t key[R > 0 ? R : 1];                // ~0 past the end
+  uint32_t key[R > 0 ? R : 1];                // ~0 past the end: no weight's key
   if constexpr (R > 0) {
     float x[R];
 #pragma unroll
@@ -93,28 +97,40 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
     }
   };
 
-  // the keep-th smallest key: digit by digit from the top
+  // The keep-th smallest key, digit by digit from the top.  The keys of the
+  // first digit's bin (some percent of them) go into a list, and the other two
+  // digits and the waves' counts come from that; a bin that the list cannot
+  // hold (many equal weights) is swept again instead.
   uint32_t prefix = 0, mask = 0;
   uint32_t want = (uint32_t)keep;             // still to find among keys matching prefix
+  int listed = -1;                            // keys in the list, -1: none built
+  int less = 0, same = 0;                     // of this wave: keys below, equal to the threshold
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
     for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    sweep([&](int t0, uint32_t k) {
-      const bool in = t0 + lane < hi && (k & mask) == prefix;
-      const uint32_t bin = (k >> shift) & bits;
-      // one count for a wave of one bin (equal weights would queue for it)
-      const uint64_t m = __builtin_amdgcn_ballot_w64(in);
-      if (m == 0) return;
-      const int first = __builtin_amdgcn_readlane((int)bin, __builtin_ctzll(m));
-      if (__builtin_amdgcn_ballot_w64(in && bin != (uint32_t)first) == 0) {
-        if (lane == 0) atomicAdd(&hist[first], (uint32_t)__builtin_popcountll(m));
-      } else if (in) {
-        atomicAdd(&hist[bin], 1u);
+    if (listed >= 0) {
+      for (int i = tid; i < listed; i += kSelThreads) {
+        const uint32_t k = list_key[i];
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1u);
       }
-    });
+    } else {
+      sweep([&](int, uint32_t k) {
+        const bool in = k != ~0u && (k & mask) == prefix;
+        const uint32_t bin = (k >> shift) & bits;
+        // one count for a wave of one bin (equal weights would queue for it)
+        const uint64_t m = __builtin_amdgcn_ballot_w64(in);
+        if (m == 0) return;
+        const int first = __builtin_amdgcn_readlane((int)bin, __builtin_ctzll(m));
+        if (__builtin_amdgcn_ballot_w64(in && bin != (uint32_t)first) == 0) {
+          if (lane == 0) atomicAdd(&hist[first], (uint32_t)__builtin_popcountll(m));
+        } else if (in) {
+          atomicAdd(&hist[bin], 1u);
+        }
+      });
+    }
     __syncthreads();
     // inclusive prefix over the bins, two per thread; the digit's bin is the
     // first whose prefix reaches want
@@ -134,28 +150,53 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(SelectArgs a)
       const bool first = want <= excl + h0;
       s_digit = (uint32_t)(2 * tid + (first ? 0 : 1));
       s_below = first ? excl : excl + h0;
+      s_count = first ? h0 : h1;
+      s_listed = 0;
     }
     __syncthreads();
     prefix |= s_digit << shift;
     mask |= bits << shift;
     want -= s_below;
+    if (pass == 0 && s_count <= (uint32_t)kSelList) {
+      const uint32_t digit = prefix >> 21;
+      sweep([&](int, uint32_t k) {
+        const bool in = k != ~0u && k >> 21 == digit;
+        less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k >> 21 < digit));
+        if (in) {
+          const int at = atomicAdd(&s_listed, 1);
+          list_key[at] = k;
+          list_wave[at] = (uint8_t)wave;
+        }
+      });
+      __syncthreads();
+      listed = s_listed;
+    }
     __syncthreads();
   }
 
   // keys below the threshold all stay, and the first `want` equal to it
-  int less = 0, same = 0;
-  sweep([&](int t0, uint32_t k) {
-    less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t0 + lane < hi && k < prefix));
-    same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t0 + lane < hi && k == prefix));
-  });
-  if (lane == 0) { s_less[wave] = less; s_same[wave] = same; }
+  if (tid < kSelWaves) { s_less[tid] = 0; s_same[tid] = 0; }
+  __syncthreads();
+  if (listed >= 0) {
+    for (int i = tid; i < listed; i += kSelThreads) {
+      if (list_key[i] < prefix) atomicAdd(&s_less[list_wave[i]], 1);
+      if (list_key[i] == prefix) atomicAdd(&s_same[list_wave[i]], 1);
+    }
+  } else {
+    less = 0;
+    sweep([&](int, uint32_t k) {
+      less += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k < prefix));
+      same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k == prefix));
+    });
+  }
+  if (lane == 0) { atomicAdd(&s_less[wave], less); atomicAdd(&s_same[wave], same); }
   __syncthreads();
   int at_less = 0, at_same = 0;
   for (int i = 0; i < wave; ++i) { at_less += s_less[i]; at_same += s_same[i]; }
   const uint64_t below = (1ull << lane) - 1ull;
   sweep([&](int t0, uint32_t k) {
     const int t = t0 + lane;
-    const bool is_less = t < hi && k < prefix, is_same = t < hi && k == prefix;
+    const bool is_less = k < prefix, is_same = k == prefix;
     const uint64_t ml = __builtin_amdgcn_ballot_w64(is_less);
     const uint64_t ms = __builtin_amdgcn_ballot_w64(is_same);
     const int rl = at_less + __builtin_popcountll(ml & below);
