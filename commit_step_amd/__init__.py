@@ -849,13 +849,19 @@ class KVCache:
             raise ValueError("num_pages and kv_heads must be positive")
         self.num_pages, self.kv_heads, self.head_dim = int(num_pages), int(kv_heads), int(head_dim)
         shape = (self.num_pages, self.kv_heads, KV_PAGE * self.head_dim)
-        self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
-        self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
-        self.k_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
-        self.v_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
-        self.device = self.k.device
-        self._c = _CCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                          self.v_scale.data_ptr(), self.num_pages, self.kv_heads, self.head_dim)
+        self._tensors = (torch.zeros(shape, dtype=torch.uint8, device=device),
+                         torch.zeros(shape, dtype=torch.uint8, device=device),
+                         torch.ones(shape[:2], dtype=torch.float32, device=device),
+                         torch.ones(shape[:2], dtype=torch.float32, device=device))
+        self.device = self._tensors[0].device
+        self._c = _CCache(*(t.data_ptr() for t in self._tensors), self.num_pages, self.kv_heads,
+                          self.head_dim)
+
+    # the pool's memory cannot be exchanged, only written: the calls hold its addresses
+    k = property(lambda self: self._tensors[0], doc="e4m3 codes of the keys (uint8)")
+    v = property(lambda self: self._tensors[1], doc="e4m3 codes of the values (uint8)")
+    k_scale = property(lambda self: self._tensors[2], doc="(num_pages, kv_heads) float32")
+    v_scale = property(lambda self: self._tensors[3], doc="(num_pages, kv_heads) float32")
 
 
 def _cache(cache):

@@ -732,6 +732,14 @@ size_t attn_workspace(int64_t rows, int splits, int64_t D) {
   return splits <= 1 ? 0 : (size_t)rows * splits * (D + 2) * 4;
 }
 
+// Sizes that the calls accept, and whose products fit 64 bits.
+bool sane_sizes(int64_t B, int64_t L, int64_t q_heads, int64_t kv_heads, int64_t max_pages) {
+  return B >= 0 && L >= 0 && q_heads >= 1 && q_heads <= 0x7fffffLL && kv_heads >= 1 &&
+         kv_heads <= 4096 && q_heads % kv_heads == 0 && max_pages >= 0 &&
+         max_pages <= 0x7fffffffLL / kPage && B <= 0x7fffffffLL && L <= 0x7fffff00LL / q_heads &&
+         (B == 0 || L * q_heads <= (1LL << 40) / B);
+}
+
 int check_attention(const char *who, const dllm_kv_cache *cache, const void *q,
                     const int64_t *q_strides, int64_t B, int64_t L, int64_t q_heads,
                     const int32_t *page_table, int64_t max_pages, int64_t table_stride,
@@ -834,7 +842,7 @@ using namespace dllm;
 extern "C" size_t dllm_block_attention_workspace_size(int64_t B, int64_t L, int64_t q_heads,
                                                       int64_t kv_heads, int64_t head_dim,
                                                       int64_t max_pages) {
-  if (B < 0 || L < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0 ||
+  if (!sane_sizes(B, L, q_heads, kv_heads, max_pages) ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   const AttnPlan p = attn_plan(B, L * (q_heads / kv_heads), kv_heads, head_dim, max_pages);
@@ -900,8 +908,7 @@ extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
 
 extern "C" size_t dllm_attention_weights_workspace_size(int64_t B, int64_t L, int64_t q_heads,
                                                         int64_t kv_heads, int64_t max_pages) {
-  if (B < 0 || L < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0)
-    return 0;
+  if (!sane_sizes(B, L, q_heads, kv_heads, max_pages)) return 0;
   const WeightPlan p = weight_plan(B, L * (q_heads / kv_heads), kv_heads, max_pages);
   return (size_t)p.parts * B * max_pages * kPage * 4;
 }

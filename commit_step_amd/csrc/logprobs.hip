@@ -661,7 +661,7 @@ using namespace dllm;
 extern "C" size_t dllm_token_logprobs_workspace_size(int dtype, int64_t B, int64_t L, int64_t V,
                                                      int top) {
   if ((dtype != DLLM_F32 && dtype != DLLM_BF16) || B < 0 || L < 0 || V < 1 || top < 0 ||
-      top > DLLM_MAX_TOP)
+      top > DLLM_MAX_TOP || (L > 0 && B > (int64_t)(0xffffffffu / 1024u) / L))
     return 0;
   const TopPlan p = top_plan(B * L, V);
   return top_workspace(B * L, p.slices, top);

@@ -436,6 +436,33 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(w1, ew) and torch.equal(w2, ew)
 
 
+def test_eviction_captured():
+    """Selection and gather in a graph, replayed over new weights and lengths."""
+    rng = np.random.default_rng(21)
+    B, H, D, T, budget = 2, 2, 64, 300, 100
+    table, new, n = _table(rng, B, 10, 4)
+    cache, ref = dc.KVCache(n, H, D), okv.Cache(n, H, D)
+    k, v = _kv(rng, B, T, H, D)
+    dc.kv_write(cache, k.cuda(), v.cuda(), _i32(table), _i32([0, 0]))
+    ref.write(_np(k), _np(v), table, [0, 0])
+    tb, nt, lens = _i32(table), _i32(new), _i32([T, T])
+    w = torch.rand((B, 320), device="cuda")
+    dc.kv_evict(cache, tb, lens, w, budget, nt, 2, 8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = dc.kv_evict(cache, tb, lens, w, budget, nt, 2, 8)
+    for i in range(4):
+        w.copy_(torch.from_numpy(rng.random((B, 320)).astype(np.float32)))
+        lens.copy_(_i32([T - 70 * i, 50 + i]))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept, nl = okv.evict_select(w.cpu().numpy(), lens.cpu().numpy(), budget, 2, 8)
+        assert np.array_equal(r.kept.cpu().numpy(), kept) and np.array_equal(r.lens.cpu().numpy(), nl)
+        ref.gather(table, kept, nl, new)
+        _same_cache(cache, ref, new, nl)
+
+
 def test_refusals_on_the_device():
     cache = dc.KVCache(4, 2, 64)
     tb, ln = _i32([[0, 1]]), _i32([10])

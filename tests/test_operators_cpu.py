@@ -140,6 +140,13 @@ def test_attention_refusals(lib):
     assert need > 0 and attend(pages=1000, stride=1000, ws=fake, wsb=need - 1) == -3
     assert attend(pages=1000, stride=1000, ws=P(260), wsb=need) == -1
     assert lib.dllm_block_attention_workspace_size(1, 1, 4, 3, 64, 10) == 0
+    big = 1 << 62                                     # products that would not fit
+    assert lib.dllm_block_attention_workspace_size(big, big, 4, 2, 64, 10) == 0
+    assert lib.dllm_attention_weights_workspace_size(1, 1, 4, 2, big) == 0
+    assert lib.dllm_token_logprobs_workspace_size(1, big, big, 8, 1) == 0
+    wide = (ctypes.c_int64 * 3)(1 << 40, 1 << 33, 64)
+    assert lib.dllm_block_attention(_c(), fake, wide, 1, 1, 4, fake, 2, 2, fake, None, None, 0, 0.1,
+                                    P(512), S3, fake, None, 0, None) == -5
     assert lib.dllm_block_attention_workspace_size(1, 1, 4, 2, 80, 10) == 0
 
 
@@ -177,6 +184,31 @@ def test_binding_refuses_cpu_tensors():
     for bad in (dict(num_pages=0), dict(kv_heads=0), dict(head_dim=96)):
         with pytest.raises(ValueError):
             dc.KVCache(**{**dict(num_pages=1, kv_heads=1, head_dim=64, device="cpu"), **bad})
+
+
+def test_pool_memory_cannot_be_exchanged():
+    """The calls hold the pool's addresses: a new tensor in its place would leave
+    them pointing at freed memory."""
+    cache = dc.KVCache(2, 1, 64, device="cpu")
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name).clone())
+
+
+@pytest.mark.parametrize("d", [1, 2, 3, 5, 7, 28, 31, 32, 33, 641, 2 ** 16, 2 ** 30 + 1, 2 ** 31 - 1])
+def test_division_by_multiplication(d):
+    """The kernels' n / d for n < 2^31 (columns by heads of a group, positions by
+    block length): the formula in attention.hip, in Python's integers."""
+    s = 0
+    while s < 31 and (1 << s) < d:
+        s += 1
+    m = ((((1 << s) - d) << 32) // d + 1) & 0xffffffff
+    ns = {0, 1, d - 1, d, d + 1, 2 ** 31 - 1, 2 ** 31 - 2}
+    ns |= {k * d + e for k in (2, 3, 1000, (2 ** 31 - 1) // d) for e in (-1, 0, 1)}
+    for n in ns:
+        if 0 <= n < 2 ** 31:
+            total = ((n * m) >> 32) + n
+            assert total < 2 ** 32 and total >> s == n // d
 
 
 SOURCES = ["logprobs.hip", "kv_cache.hip", "attention.hip", "evict.hip"]
