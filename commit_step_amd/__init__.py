@@ -672,7 +672,7 @@ def _same(t, name, dtype, shape, device):
 def _launch(device, what, fn, *args):
     """fn(*args, the device's current stream), with that device current."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -875,14 +875,15 @@ def _cache(cache):
 def _table(t, name, B, device):
     """A (B, pages) int32 page table, rows of unit stride (a slice of a larger
     table will do); returns (pages, row stride)."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and \
+            t.dim() == 2 and t.is_contiguous() and (B is None or t.shape[0] == B):
+        return t.shape[1], t.shape[1]
     _dev(t, name)
     if t.dtype is not torch.int32 or t.dim() != 2 or t.device != device:
         raise ValueError(f"{name} must be a (B, pages) int32 tensor on {device}")
     rows, pages = t.shape
     if B is not None and rows != B:
         raise ValueError(f"{name} has {rows} rows, not {B}")
-    if t.is_contiguous():
-        return pages, pages
     if pages > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} rows must have unit stride")
     return pages, t.stride(0) if rows > 1 else pages
@@ -1035,12 +1036,18 @@ def evict_select(weights, kv_lens, budget, sink=0, recent=0, new_T=None):
     if budget < 1:
         raise ValueError("budget must be positive")
     new_T = budget if new_T is None else int(new_T)
+    return _select(weights, B, T, weights.stride(0) if B > 1 else T, n, budget, int(sink),
+                   int(recent), new_T)
+
+
+def _select(weights, B, T, stride, lens_p, budget, sink, recent, new_T):
+    dev = weights.device
     kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
     lens = torch.empty((B,), dtype=torch.int32, device=dev)
     new_w = torch.empty((B, new_T), dtype=torch.float32, device=dev)
     _launch(dev, "dllm_evict_select", load_library().dllm_evict_select, weights.data_ptr(), B, T,
-            weights.stride(0) if B > 1 else T, n, budget, int(sink), int(recent), kept.data_ptr(),
-            lens.data_ptr(), new_w.data_ptr(), new_T)
+            stride, lens_p, budget, sink, recent, kept.data_ptr(), lens.data_ptr(),
+            new_w.data_ptr(), new_T)
     return Evicted(kept, lens, new_w)
 
 
@@ -1067,15 +1074,21 @@ def kv_evict(cache, page_table, kv_lens, weights, budget, new_pages, sink=0, rec
     pages are then free.  Returns Evicted: the kept positions, the new lengths,
     and the kept tokens' weights (B, KV_PAGE * new_pages.shape[1]), which go on
     accumulating."""
-    dev, _ = _cache(cache)
-    pages, _ = _table(page_table, "page_table", None, dev)
+    dev, c = _cache(cache)
+    pages, stride = _table(page_table, "page_table", None, dev)
     B = page_table.shape[0]
-    npages, _ = _table(new_pages, "new_pages", B, dev)
-    if npages * KV_PAGE < int(budget):
+    npages, nstride = _table(new_pages, "new_pages", B, dev)
+    budget, T = int(budget), pages * KV_PAGE
+    if budget < 1:
+        raise ValueError("budget must be positive")
+    if npages * KV_PAGE < budget:
         raise ValueError("new_pages cannot hold budget tokens")
-    if new_pages.data_ptr() == page_table.data_ptr() and pages:
+    table_p, new_p = page_table.data_ptr(), new_pages.data_ptr()
+    if new_p == table_p and pages:
         raise ValueError("new_pages is the page table")
-    _same(weights, "weights", torch.float32, (B, pages * KV_PAGE), dev)
-    r = evict_select(weights, kv_lens, budget, sink, recent, new_T=npages * KV_PAGE)
-    kv_gather(cache, page_table, r.kept, r.lens, new_pages)
+    _same(weights, "weights", torch.float32, (B, T), dev)
+    r = _select(weights, B, T, T, _ints(kv_lens, "kv_lens", B, dev), budget, int(sink),
+                int(recent), npages * KV_PAGE)
+    _launch(dev, "dllm_kv_gather", load_library().dllm_kv_gather, c, B, table_p, pages, stride,
+            r.kept.data_ptr(), budget, r.lens.data_ptr(), new_p, npages, nstride)
     return r
