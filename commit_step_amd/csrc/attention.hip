@@ -23,7 +23,8 @@
 // A workgroup is CW column waves times KW token waves: the column waves read
 // the same pages (from the CU's cache), the token waves take turns at the pages
 // and join through LDS.  When that leaves CUs idle the cache is also split
-// along its tokens over workgroups, and a second kernel joins the parts.
+// along its tokens over workgroups, as evenly as the sequences' lengths allow
+// (share_of), and a second kernel joins the parts.
 #include <string.h>
 
 #include <algorithm>
@@ -82,19 +83,95 @@ struct AttnArgs {
   int H, G, L;
   int ncols;                // L * G
   int groups;               // column groups (workgroups per sequence, head and split)
-  int splits;
+  int slots;                // shares of the sequences, over all of them: B, no splits, or more
+  int min_pages;            // of a share, unless its sequence has less
   int vec;                  // query rows are 16-byte aligned
   int out_vec;              // output rows are 8-byte aligned
   float c;                  // scale * log2 e
   float *lse;
-  float *part_o;            // [B * H * ncols][splits][D]
-  float *part_ml;           // [B * H * ncols][splits][2]
+  float *part_o;            // [slots][H * ncols][D]
+  float *part_ml;           // [slots][H * ncols][2]
+  int2 *part_of;            // [B]: a sequence's first slot and number of slots
   // dllm_attention_weights
   float *weights;
   float *part_w;            // [parts][B][T]
   int parts, shares;        // H * shares
   int token_groups;
 };
+
+// What a workgroup takes of the tokens: share `split` of the `splits` even ones
+// of sequence b (b < 0: nothing), whose length is len.
+struct Share { int b, split, splits, len; };
+
+constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
+
+constexpr int kShareLanes = 8;           // sequences a lane looks after: splits need B <= 512
+
+// The share in slot `slot`.  Lengths are on the device, so every workgroup works
+// the division out for itself: with `per` pages a share, the smallest (within a
+// sixteenth) for which the slots suffice, sequence b has ceil(pages_b / per)
+// shares, one if it is empty, and their slots follow each other in the order of
+// b.  The slots suffice for per >= total / (slots - B): at most B shares are not
+// full.  Eight lengths of 32768 and seven times 500 take 27 us so, against 46 us
+// with as many shares for each; equal ones take up to 1.6 us more (24 of 2000).
+__device__ __forceinline__ Share share_of(const AttnArgs &a, int slot) {
+  const int lane = threadIdx.x & 63;
+  int len[kShareLanes] = {};
+  float pages[kShareLanes];
+#pragma unroll
+  for (int j = 0; j < kShareLanes; ++j)
+    if (j * 64 < a.B) len[j] = a.kv_lens[min((int64_t)(j * 64 + lane), a.B - 1)];
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < kShareLanes; ++j) {
+    // 2^22 pages are as long as any for this purpose: sums fit 31 bits, and
+    // page counts are exact in float32
+    const int64_t n = (cut_len(len[j], a.max_pages) + kPage - 1) / kPage;
+    const int m = j * 64 + lane < a.B ? (int)min(n, (int64_t)(1 << 22) - 1) : 0;
+    pages[j] = (float)m;
+    sum += m;
+  }
+  const float total = (float)wave_sum_i(sum);
+  // ceil(n / per), or one, as 1 + floor(n r): r is below 1 / per, by more than
+  // the roundings here and by too little to matter
+  constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
+  auto shares = [&](int j, float r) { return j * 64 + lane < a.B ? 1 + (int)(pages[j] * r) : 0; };
+  int lo = max(a.min_pages, (int)(total * __builtin_amdgcn_rcpf((float)a.slots)));
+  int hi = max(lo, (int)(total * __builtin_amdgcn_rcpf((float)(a.slots - (int)a.B)) * kAbove) + 1);
+  while (hi - lo > hi / 16) {
+    const int mid = (lo + hi) / 2;
+    const float r = __builtin_amdgcn_rcpf((float)mid) * kBelow;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < kShareLanes; ++j)
+      if (j * 64 < a.B) count += shares(j, r);
+    if (wave_sum_i(count) <= a.slots) hi = mid;
+    else lo = mid + 1;
+  }
+  const float r = __builtin_amdgcn_rcpf((float)hi) * kBelow;
+  int before = 0;                        // slots of the sequences before these 64
+#pragma unroll
+  for (int j = 0; j < kShareLanes; ++j)
+    if (j * 64 < a.B) {
+      const int mine = shares(j, r);
+      int to = mine;                     // slots up to and with this lane's
+      to += dpp_i<kRowShr1>(0, to);
+      to += dpp_i<kRowShr2>(0, to);
+      to += dpp_i<kRowShr4>(0, to);
+      to += dpp_i<kRowShr8>(0, to);
+      to += dpp_i<kRowBcast15, 0xA>(0, to);
+      to += dpp_i<kRowBcast31, 0xC>(0, to);
+      const int at = slot - before;
+      const uint64_t in = __builtin_amdgcn_ballot_w64(at >= to - mine && at < to);
+      if (in != 0) {
+        const int i = __builtin_ctzll(in), n = __builtin_amdgcn_readlane(mine, i);
+        return {__builtin_amdgcn_readfirstlane(j * 64 + i),
+                at - (__builtin_amdgcn_readlane(to, i) - n), n, __builtin_amdgcn_readlane(len[j], i)};
+      }
+      before += __builtin_amdgcn_readlane(to, 63);
+    }
+  return {-1, 0, 1, 0};
+}
 
 // The columns of one wave tile: lane i of each half is column c0 + i.
 struct Column {
@@ -255,12 +332,12 @@ __device__ __forceinline__ void accumulate(const u32x4 (&vw)[D / 32], const f16x
 
 // Columns' results: the output itself, or this split's part.
 template <int D>
-__device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv, int64_t c, int split,
+__device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv, int64_t c, int slot,
                                            const Column &col, const Tile<D> &t) {
   const int h = (threadIdx.x & 63) >> 5;
   const float l = halves_sum(t.l);
   if (!col.on) return;
-  if (a.splits == 1) {
+  if (a.slots == a.B) {
     const float inv = l > 0.f ? 1.0f / l : (l == l ? 0.f : l);
     const int64_t head = (int64_t)hkv * a.G + col.g;
     uint16_t *o = a.out + b * a.os[0] + col.l * a.os[1] + head * a.os[2];
@@ -284,7 +361,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv
       a.lse[lse_at(a, b, hkv, col)] = log_sum(t.m, l);
     return;
   }
-  const int64_t row = ((b * a.H + hkv) * a.ncols + c) * a.splits + split;
+  const int64_t row = ((int64_t)slot * a.H + hkv) * a.ncols + c;
   float *po = a.part_o + row * D;
 #pragma unroll
   for (int cc = 0; cc < D / 32; ++cc)
@@ -322,12 +399,20 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
   }
   const int group = a.groups - 1 - (int)(unit % (uint32_t)a.groups);
   unit /= (uint32_t)a.groups;
-  const int split = (int)(unit % (uint32_t)a.splits);
-  unit /= (uint32_t)a.splits;
   const int hkv = (int)(unit % (uint32_t)a.H);
-  const int64_t b = unit / (uint32_t)a.H;
+  const int slot = (int)(unit / (uint32_t)a.H);
+  Share share = {slot, 0, 1, 0};
+  if (a.slots == a.B) {
+    share.len = a.kv_lens[slot];
+  } else {
+    share = share_of(a, slot);
+    if (share.b < 0) return;
+  }
+  const int64_t b = share.b;
+  if (a.slots != a.B && share.split == 0 && hkv == 0 && group == 0 && threadIdx.x == 0)
+    a.part_of[b] = make_int2(slot, share.splits);
   const int64_t c0 = ((int64_t)group * CW + cw) * 32;
-  const int n = (int)cut_len(a.kv_lens[b], a.max_pages);
+  const int n = (int)cut_len(share.len, a.max_pages);
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
 
   const Column col = column(a, b, c0 + (lane & 31), n, q_len);
@@ -343,8 +428,8 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
   tile.m = kNegInf;
   tile.l = 0.f;
   const int pages = (max_lim + kPage - 1) / kPage;
-  const int per = (pages + a.splits - 1) / a.splits;
-  const int lo = split * per, hi = min(lo + per, pages);
+  const int per = (pages + share.splits - 1) / share.splits;
+  const int lo = share.split * per, hi = min(lo + per, pages);
   const int32_t *row = a.table + b * a.table_stride;
   // This wave's pages are lo + kw_id + KW i.  Lane j of the directory knows page
   // i = 64 c + j of the current run of 64: no scalar load, with its wait for
@@ -496,10 +581,10 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
     }
     if (kw_id != 0) return;
   }
-  store_tile<D>(a, b, hkv, c0 + (lane & 31), split, col, tile);
+  store_tile<D>(a, b, hkv, c0 + (lane & 31), slot, col, tile);
 }
 
-// One wave per query and head: joins the splits' parts in split order.
+// One wave per query and head: joins the shares' parts in their order.
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;
@@ -512,20 +597,23 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   const int l = (int)(c / a.G), g = (int)(c % a.G);
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
   if (l >= q_len) return;
-  const float *ml = a.part_ml + row * a.splits * 2;
+  const int2 of = a.part_of[b];
+  const int64_t step = (int64_t)a.H * a.ncols, first = of.x * step + hkv * (int64_t)a.ncols + c;
+  const float *ml = a.part_ml + first * 2;
   float m = kNegInf;
-  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[2 * s]);
+  for (int s = lane; s < of.y; s += 64) m = fmaxf(m, ml[s * step * 2]);
   m = wave_max(m);
-  const float *po = a.part_o + row * a.splits * D + lane * PER;
+  const float *po = a.part_o + first * D + lane * PER;
   float acc[PER], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float ms = ml[2 * s];
+#pragma unroll 4
+  for (int s = 0; s < of.y; ++s) {
+    const float ms = ml[s * step * 2];
     const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - m);
-    sum = fmaf(ml[2 * s + 1], f, sum);
+    sum = fmaf(ml[s * step * 2 + 1], f, sum);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(po[(int64_t)s * D + e], f, acc[e]);
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(po[s * step * D + e], f, acc[e]);
   }
   const float inv = sum > 0.f ? 1.0f / sum : (sum == sum ? 0.f : sum);
   const int64_t head = (int64_t)hkv * a.G + g;
@@ -703,7 +791,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_weights_join_kernel(At
 
 struct AttnPlan {
   int cw, kw;      // column waves, token waves
-  int groups, splits;
+  int groups, slots, min_pages;
 };
 
 // 8 waves a workgroup (2 a SIMD at up to 256 registers; head_dim 256 needs 512,
@@ -719,17 +807,21 @@ AttnPlan attn_plan(int64_t B, int64_t ncols, int64_t H, int64_t D, int64_t max_p
   const int64_t units = std::max<int64_t>(1, B * H * p.groups);
   p.kw = (D == 256 ? 4 : 8) / p.cw;
   if (p.cw == 4 && units >= 2 * cus) p.kw = 1;
-  // split the tokens until every CU has its workgroups, with 2 pages or more
-  // per token wave and 4 or more per split
-  const int64_t want = (p.cw * p.kw == 8 ? 1 : 2) * cus;
-  int64_t s = (want + units - 1) / units;
-  s = std::min<int64_t>(s, max_pages / std::max(2 * p.kw, 4));
-  p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, s), 128);
+  // Split the tokens until every CU has its workgroups at once (twice that where
+  // less than two shares a sequence come out of it: then longer sequences can
+  // have more than one), with 2 pages or more per token wave and 4 or more per
+  // share.
+  const int64_t want = (p.cw * p.kw == 8 ? 1 : 2) * cus, rest = H * p.groups;
+  p.min_pages = std::max(2 * p.kw, 4);
+  int64_t s = want / rest;
+  if (s > B && s < 2 * B) s *= 2;
+  s = std::min({s, B * (max_pages / p.min_pages), B + 127});
+  p.slots = (int)(B > 64 * kShareLanes ? B : std::max(s, B));
   return p;
 }
 
-size_t attn_workspace(int64_t rows, int splits, int64_t D) {
-  return splits <= 1 ? 0 : (size_t)rows * splits * (D + 2) * 4;
+size_t attn_workspace(const AttnPlan &p, int64_t B, int64_t cols, int64_t D) {
+  return p.slots == B ? 0 : (size_t)p.slots * cols * (D + 2) * 4 + (size_t)B * sizeof(int2);
 }
 
 // Sizes that the calls accept, and whose products fit 64 bits.
@@ -846,7 +938,7 @@ extern "C" size_t dllm_block_attention_workspace_size(int64_t B, int64_t L, int6
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   const AttnPlan p = attn_plan(B, L * (q_heads / kv_heads), kv_heads, head_dim, max_pages);
-  return attn_workspace(B * L * q_heads, p.splits, head_dim);
+  return attn_workspace(p, B, L * q_heads, head_dim);
 }
 
 extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
@@ -871,12 +963,12 @@ extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
   const int D = cache->head_dim;
   const AttnPlan p = attn_plan(B, a.ncols, a.H, D, max_pages);
   const int64_t rows = B * L * q_heads;
-  const size_t need = attn_workspace(rows, p.splits, D);
+  const size_t need = attn_workspace(p, B, L * q_heads, D);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(DLLM_ERR_SHAPE, "%s: workspace has %zu bytes, needs %zu", who, workspace_bytes, need);
   if (need > 0 && (uintptr_t)workspace % 16 != 0)
     return fail(DLLM_ERR_ARG, "%s: workspace must be 16-byte aligned", who);
-  const int64_t wgs = B * a.H * p.groups * p.splits;
+  const int64_t wgs = (int64_t)p.slots * a.H * p.groups;
   if (wgs > 0xffffffffLL / 512 || (rows + kJoinWaves - 1) / kJoinWaves > 0xffffffffLL / kJoinThreads)
     return fail(DLLM_ERR_UNSUPPORTED, "%s: too many queries in one call", who);
   a.out = (uint16_t *)out;
@@ -887,15 +979,20 @@ extern "C" int dllm_block_attention(const dllm_kv_cache *cache, const void *q,
   }
   a.lse = lse;
   a.groups = p.groups;
-  a.splits = p.splits;
-  a.part_o = (float *)workspace;
-  a.part_ml = (float *)workspace + (need > 0 ? rows * p.splits * D : 0);
+  a.slots = p.slots;
+  a.min_pages = p.min_pages;
+  if (need > 0) {
+    const int64_t part_rows = (int64_t)p.slots * L * q_heads;
+    a.part_o = (float *)workspace;
+    a.part_ml = a.part_o + part_rows * D;
+    a.part_of = (int2 *)(a.part_ml + part_rows * 2);
+  }
   const dim3 grid((uint32_t)wgs);
   if (D == 64) launch_attention<64>(p, a, grid, stream);
   else if (D == 128) launch_attention<128>(p, a, grid, stream);
   else launch_attention<256>(p, a, grid, stream);
   const int st = check_launch(who);
-  if (st != DLLM_OK || p.splits == 1) return st;
+  if (st != DLLM_OK || p.slots == B) return st;
   const dim3 jgrid((uint32_t)((rows + kJoinWaves - 1) / kJoinWaves));
   if (D == 64)
     hipLaunchKernelGGL(attention_join_kernel<64>, jgrid, dim3(kJoinThreads), 0, stream, a);

@@ -284,6 +284,47 @@ def test_attention_long_split_and_ragged():
         assert not r.out[3].any() and not r.out[1, qn[1]:].any()
 
 
+@pytest.mark.parametrize("B,H,G,D,T", [(1, 1, 1, 64, 5000), (3, 2, 9, 128, 3000), (70, 1, 2, 64, 2100),
+                                       (130, 1, 1, 128, 1100), (300, 1, 1, 256, 520), (600, 1, 1, 256, 300)])
+@pytest.mark.parametrize("kind", ["one long", "halves", "any"])
+def test_attention_lengths_of_one_batch(B, H, G, D, T, kind):
+    """Sequences of one cache prefix, of lengths far apart: however the tokens
+    are shared out, every sequence's result is its own."""
+    rng = np.random.default_rng(B + T)
+    lens = {"one long": np.full(B, 5), "halves": np.where(np.arange(B) % 2, T, T // 2),
+            "any": rng.integers(0, T + 1, B)}[kind]
+    if kind == "one long":
+        lens[B // 2] = T
+    pages = -(-T // PAGE)
+    cache, ref = dc.KVCache(pages, H, D), okv.Cache(pages, H, D)
+    k, v = _kv(rng, 1, T, H, D)
+    one = np.arange(pages, dtype=np.int32)[::-1].copy()[None]
+    dc.kv_write(cache, k.cuda(), v.cuda(), _i32(one), _i32([0]))
+    ref.write(_np(k), _np(v), one, [0])
+    rk, rv = (x[0, :T] for x in ref.read(one, [T]))              # (T, H, D)
+    q = _bf16(rng.normal(0, 1, (B, 1, H * G, D)) * 4 / np.abs(rk).max())
+    r = dc.block_attention(q.cuda(), cache, _i32(one.repeat(B, 0)), _i32(lens))
+    out, lse = _np(r.out)[:, 0].reshape(B, H, G, D), _np(r.lse).reshape(B, H, G)
+    qd, scale = _np(q)[:, 0].reshape(B, H, G, D), D ** -0.5
+    live = np.arange(T)[None] < lens[:, None]                    # (B, T)
+    for h in range(H):
+        s = scale * (qd[:, h] @ rk[:, h].T)                      # (B, G, T)
+        ds = (D + 8) * U * scale * (np.abs(qd[:, h]) @ np.abs(rk[:, h]).T).max() + 4 * U * np.abs(s).max()
+        s = np.where(live[:, None], s, -np.inf)
+        m = np.maximum(s.max(-1, keepdims=True), -1e300)
+        e = np.exp(s - m)
+        z = e.sum(-1, keepdims=True)
+        p = e / np.maximum(z, 1e-300)
+        o, mass = p @ rv[:, h], p @ np.abs(rv[:, h])
+        tol = 2.0 ** -8 * np.abs(o) + mass * (2.0 ** -11 + 2 * ds + (T + 40) * U) * 1.01 \
+            + 2.0 ** -38 * T * np.abs(rv).max()
+        assert (np.abs(out[:, h] - o) <= tol).all(), (np.abs(out[:, h] - o) - tol).max()
+        some = lens > 0
+        want = (m + np.log(np.maximum(z, 1e-300)))[..., 0]
+        assert (np.abs(lse[some, h] - want[some]) <= ds + (T + 40) * U + 4 * U * np.abs(want[some])).all()
+        assert (lse[~some] == -np.inf).all() and not out[~some].any()
+
+
 def test_attention_rows_past_q_lens_are_left():
     cache, ref, table, q, n = _attention_case(1, 2, 4, 2, 2, 64, 70, [70, 9])
     for lens in ([70, 9],):
