@@ -3,7 +3,11 @@
 // All three move data: one workgroup per page and head, 16-byte loads and
 // stores, the transposition between tokens-by-channels and the values' layout
 // through LDS.  Bound by HBM bandwidth (a write reads 4 D bytes per token and
-// head and stores 2 D; a read the reverse).
+// head and stores 2 D; a read the reverse) and, for a few tokens, by the launch
+// and two dependent fetches.  Measured at 32000 tokens of 8 heads of 128
+// channels: a write 50 us (3.9 TB/s: two sweeps over a page in LDS between load
+// and store, the second after the page's maximum is known), a read 31 us
+// (6.4 TB/s); 8 tokens of 4 heads: 5.5 and 4 us.
 #include <string.h>
 
 #include <algorithm>
@@ -255,6 +259,9 @@ struct GatherArgs {
 // lie one byte in every 16-byte piece, so each old page that a kept token comes
 // from is read whole (its other kept tokens are neighbours) and the lane picks
 // its bytes; kept positions increase, so an old page is met once per new page.
+// The values' layout, which makes attention's loads contiguous, is paid for
+// here: a quarter of 106496 tokens of 8 heads of 128 channels takes 77 us, for
+// 134 MB that have to move and about 335 MB that do.
 template <int D>
 __global__ __launch_bounds__(kKvThreads) void kv_gather_kernel(GatherArgs a) {
   constexpr int KI = (D / 16 * kPage + kKvThreads - 1) / kKvThreads;   // key items per thread

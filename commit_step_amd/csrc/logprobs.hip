@@ -4,10 +4,14 @@
 // running maximum M, z- and S of token_stats_dev.h (chunk_update), and the
 // candidates for the K largest logits.  Then
 //   log p_t = (x_t - M) / T - log1p(z-),   H = log1p(z-) - ln2 S / (1 + z-).
-// Bound by reading the logits once from HBM.
+// Bound by reading the logits once from HBM: 1024 rows of 151936 bfloat16 with 5
+// alternatives take 69.5 us (4.5 TB/s), 2048 of 126464 without any 111 us
+// (4.7 TB/s); one row, split over 30 workgroups, 14 us with 20 alternatives.
 //
 // Backward, per scored position: p_v from the logits and the forward pass's
-// (M, log z), one read and one write of the row; nothing is summed.
+// (M, log z), one read and one write of the row; nothing is summed.  Rows that
+// are not scored are written without being read.  4096 rows of 126464, half of
+// them scored, take 316 us (4.9 TB/s, the rate of a large copy).
 #include <string.h>
 
 #include <algorithm>

@@ -550,8 +550,9 @@ int dllm_kv_read(const dllm_kv_cache *cache, int64_t B, const int32_t *page_tabl
  * that attends to nothing gives out = 0, lse = -inf.
  *   q        (B, L, q_heads, head_dim) bfloat16, element strides q_strides[3]
  *            (HOST) of the first three dimensions, unit stride along the
- *            last; q_heads a multiple of kv_heads, query head h reading
- *            key/value head h / (q_heads / kv_heads).
+ *            last, those of the second and third within 32 bits; q_heads a
+ *            multiple of kv_heads, query head h reading key/value head
+ *            h / (q_heads / kv_heads).
  *   q_start  positions of the first queries, or NULL (0); used by block_len
  *            only; a negative one counts as 0.
  *   q_lens   queries of each sequence, or NULL (L): outputs of queries
@@ -564,7 +565,9 @@ int dllm_kv_read(const dllm_kv_cache *cache, int64_t B, const int32_t *page_tabl
  *            share one.
  * Products of a query and a key are exact and summed in float32; a weight is
  * rounded to 11 bits before it multiplies the value, and the sums of weights
- * and values are float32. */
+ * and values are float32.  Their order follows the lengths of the whole batch
+ * and max_pages: the same call gives the same bits, another batch may round a
+ * sequence's sums differently. */
 int dllm_block_attention(const dllm_kv_cache *cache, const void *q, const int64_t *q_strides,
                          int64_t B, int64_t L, int64_t q_heads, const int32_t *page_table,
                          int64_t max_pages, int64_t table_stride, const int32_t *kv_lens,
