@@ -791,6 +791,16 @@ class _LogprobsFunction(torch.autograd.Function):
         return grad, None, None, None, None, None
 
 
+def _check_leaf(node, device):
+    """node: a leaf's gradient accumulator, which all living graphs of the leaf
+    share and which runs on the stream it was made on, noted here."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if node.metadata.setdefault("commit_step_amd", stream) != stream and _capturing(device):
+        raise RuntimeError("the captured backward pass of a leaf would meet an autograd graph of "
+                           "it that lives on another stream; let that go first, or capture "
+                           "token_logprobs_grad")
+
+
 def token_logprobs(logits, targets, temperature=1.0, suppress_ids=(), top=0, workspace=None):
     """Scores of given tokens: for (B, L, V) float32 / bfloat16 logits and (B, L)
     int32 targets, log softmax(logits / temperature) at the target, the
@@ -803,10 +813,19 @@ def token_logprobs(logits, targets, temperature=1.0, suppress_ids=(), top=0, wor
     require one.  ``norm`` (B, L, 2) is what token_logprobs_grad takes.
     ``workspace``: None, or a zero-filled uint8 tensor that no other call in
     flight uses.
+
+    Under graph capture a leaf's backward pass is refused while an autograd graph
+    of the same leaf, made on another stream, lives: torch would join that stream
+    to the capture and fail in its own thread.  (The same holds for a model's
+    parameters, which this call does not see.)  token_logprobs_grad has no such
+    tie.
     """
     if torch.is_grad_enabled() and isinstance(logits, torch.Tensor) and logits.requires_grad:
-        return Logprobs(*_LogprobsFunction.apply(logits, targets, temperature, suppress_ids, top,
-                                                 workspace))
+        r = Logprobs(*_LogprobsFunction.apply(logits, targets, temperature, suppress_ids, top,
+                                              workspace))
+        if logits.is_leaf:
+            _check_leaf(r.logprob.grad_fn.next_functions[0][0], logits.device)
+        return r
     return _logprobs_call(logits, targets, temperature, suppress_ids, top, workspace)
 
 
@@ -905,6 +924,17 @@ def _heads(t, name, shape, device):
     return _Strides(st[0], st[1], st[2])
 
 
+def _apart(t, name):
+    """Refuses an output whose elements share memory (an expanded view)."""
+    if isinstance(t, torch.Tensor) and not t.is_contiguous():
+        reach = 1
+        for stride, size in sorted(zip(t.stride(), t.shape)):
+            if size > 1:
+                if stride < reach:
+                    raise ValueError(f"{name} has elements that share memory")
+                reach += stride * (size - 1)
+
+
 def _ints(t, name, B, device):
     return None if t is None else _same(t, name, torch.int32, (B,), device).data_ptr()
 
@@ -990,6 +1020,8 @@ def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, bl
     if out is None:
         out = (torch.empty if q_lens is None else torch.zeros)(shape, dtype=torch.bfloat16,
                                                                 device=dev)
+    else:
+        _apart(out, "out")
     os_ = _heads(out, "out", shape, dev)
     if lse is None:
         lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)

@@ -124,10 +124,10 @@ __device__ __forceinline__ Share share_of(const AttnArgs &a, int slot) {
   int sum = 0;
 #pragma unroll
   for (int j = 0; j < kShareLanes; ++j) {
-    // 2^22 pages are as long as any for this purpose: sums fit 31 bits, and
-    // page counts are exact in float32
+    // 2^21 pages are as long as any for this purpose: sums stay within 2^30,
+    // and page counts are exact in float32
     const int64_t n = (cut_len(len[j], a.max_pages) + kPage - 1) / kPage;
-    const int m = j * 64 + lane < a.B ? (int)min(n, (int64_t)(1 << 22) - 1) : 0;
+    const int m = j * 64 + lane < a.B ? (int)min(n, (int64_t)(1 << 21) - 1) : 0;
     pages[j] = (float)m;
     sum += m;
   }
@@ -871,8 +871,8 @@ int check_attention(const char *who, const dllm_kv_cache *cache, const void *q,
   if (rc != DLLM_OK) return rc;
   if (block_len < 0 || block_len > 0x7fffffffLL)
     return fail(DLLM_ERR_ARG, "%s: block_len must be in [0, 2^31)", who);
-  if (!(scale > 0.0f) || scale == __builtin_inff())
-    return fail(DLLM_ERR_ARG, "%s: scale must be finite and > 0", who);
+  if (!(scale > 0.0f) || !(scale <= 0x1p127f))
+    return fail(DLLM_ERR_ARG, "%s: scale must be > 0 and at most 2^127", who);
   if (B == 0 || L == 0) return DLLM_OK;
   if (!q || !q_strides || !kv_lens)
     return fail(DLLM_ERR_ARG, "%s: q, q_strides and kv_lens must be non-NULL", who);

@@ -243,9 +243,9 @@ extern "C" int dllm_evict_select(const float *weights, int64_t B, int64_t T,
   if (B > 0xffffffffLL / kSelThreads)
     return fail(DLLM_ERR_UNSUPPORTED, "%s: too many sequences in one call", who);
   if (B == 0) return ok();
-  if (!weights || !kv_lens || !kept || !new_lens)
+  if ((!weights && T > 0) || !kv_lens || !kept || !new_lens)
     return fail(DLLM_ERR_ARG, "%s: weights, kv_lens, kept and new_lens must be non-NULL", who);
-  if ((const void *)new_weights == (const void *)weights)
+  if (weights && (const void *)new_weights == (const void *)weights)
     return fail(DLLM_ERR_ARG, "%s: new_weights aliases weights", who);
   const SelectArgs a{weights, weights_stride, T, budget, sink, recent, new_T,
                      kv_lens, kept, new_lens, new_weights};

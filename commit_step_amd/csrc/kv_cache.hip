@@ -523,7 +523,7 @@ extern "C" int dllm_kv_gather(const dllm_kv_cache *cache, int64_t B, const int32
   if (rc != DLLM_OK) return rc;
   if (kept_stride < 0) return fail(DLLM_ERR_ARG, "%s: kept_stride must be >= 0", who);
   if (B == 0 || new_pages == 0) return ok();
-  if (!kept || !counts || (max_pages > 0 && page_table == new_table))
+  if ((!kept && kept_stride > 0) || !counts || (max_pages > 0 && page_table == new_table))
     return fail(DLLM_ERR_ARG, "%s: kept and counts must be non-NULL, and new_table another table",
                 who);
   rc = check_units(who, B, new_pages, cache->kv_heads);

@@ -631,8 +631,8 @@ int check_common(const char *who, const void *logits, int dtype, int64_t B, int6
   if (V < 1 || V > 0x7fffffffLL)
     return fail(DLLM_ERR_ARG, "%s: V = %lld must be in [1, 2^31)", who, (long long)V);
   if (row_stride < V) return fail(DLLM_ERR_ARG, "%s: row_stride < V", who);
-  if (!(temperature > 0.0f) || temperature == __builtin_inff())
-    return fail(DLLM_ERR_ARG, "%s: temperature must be finite and > 0", who);
+  if (!(temperature >= 0x1p-126f) || temperature == __builtin_inff())
+    return fail(DLLM_ERR_ARG, "%s: temperature must be finite and at least 2^-126", who);
   if (n_suppress < 0 || n_suppress > DLLM_MAX_SUPPRESS)
     return fail(DLLM_ERR_ARG, "%s: n_suppress must be in [0, %d]", who, DLLM_MAX_SUPPRESS);
   if (n_suppress > 0 && !suppress_ids)

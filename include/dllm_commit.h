@@ -422,7 +422,7 @@ int dllm_stable_confident_stop(const int32_t *argmax, const float *entropy,
  *       logit: what dllm_token_logprobs_grad needs of the forward pass.
  *
  *   logits, dtype, row_stride, suppress_ids  as in dllm_token_stats.
- *   temperature  finite, > 0.
+ *   temperature  finite, at least 2^-126 (its reciprocal is finite).
  *   targets      (B, L) int32 DEVICE.  A target outside [0, V) marks a
  *                position that is not scored: its logits are not read, its
  *                logprob and entropy are 0, its alternatives (-1, -inf), its
@@ -557,7 +557,7 @@ int dllm_kv_read(const dllm_kv_cache *cache, int64_t B, const int32_t *page_tabl
  *            only; a negative one counts as 0.
  *   q_lens   queries of each sequence, or NULL (L): outputs of queries
  *            l >= q_lens[b] are left as they were.
- *   scale    finite, > 0.
+ *   scale    > 0, at most 2^127.
  *   out      as q, bfloat16, element strides out_strides[3]; must not overlap q.
  *   lse      (B, q_heads, L) float32, natural log.
  *   workspace at least dllm_block_attention_workspace_size() bytes, 16-byte

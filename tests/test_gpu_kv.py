@@ -520,7 +520,8 @@ def test_refusals_on_the_device():
                 dict(kv_lens=ln.long()), dict(block_len=-1), dict(scale=0.0), dict(scale=float("nan")),
                 dict(weights=torch.zeros((1, 63), device="cuda")), dict(out=q), dict(out=q.float()),
                 dict(lse=torch.zeros((1, 4, 3), device="cuda")), dict(q_lens=ln.cpu()),
-                dict(page_table=_i32([[0, 1, 2, 3]])[:, ::2])):
+                dict(page_table=_i32([[0, 1, 2, 3]])[:, ::2]),
+                dict(out=torch.zeros_like(q[:, :1]).expand(1, 4, 4, 64))):
         with pytest.raises(ValueError):
             dc.block_attention(**{**good, **bad})
     w = torch.zeros((1, 64), device="cuda")
@@ -534,3 +535,6 @@ def test_refusals_on_the_device():
     assert r.out.shape == (1, 0, 4, 64) and r.lse.shape == (1, 4, 0)
     dc.kv_write(cache, x[:, :0], x[:, :0], tb, ln)
     assert dc.block_attention(q, cache, tb[:, :0], ln).lse.isneginf().all()
+    e = dc.kv_evict(cache, tb[:, :0], ln, w[:, :0], 16, _i32([[2]]))
+    assert int(e.lens) == 0 and (e.kept == -1).all() and not e.weights.any()
+    dc.kv_gather(cache, tb, e.kept[:, :0], e.lens, _i32([[3]]))

@@ -253,6 +253,34 @@ def test_other_stream_and_graph():
         assert torch.equal(eg, gx) and torch.equal(eg, gx2)
 
 
+def test_captured_backward_beside_a_living_graph_of_the_leaf():
+    x = torch.randn((1, 2, 300), device="cuda", requires_grad=True)
+    t = torch.tensor([[5, -1]], dtype=torch.int32, device="cuda")
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def step():
+        return torch.autograd.grad(dc.token_logprobs(x, t).logprob.sum(), x)[0]
+
+    alive = dc.token_logprobs(x, t)                    # on the current stream
+    want = torch.autograd.grad(alive.logprob.sum(), x, retain_graph=True)[0]
+    with torch.cuda.stream(st):
+        assert torch.equal(step(), want)               # eager: streams may differ
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        with pytest.raises(RuntimeError, match="lives on another stream"):
+            dc.token_logprobs(x, t)
+        dc.token_logprobs(x.detach(), t)               # no backward pass: no tie
+    del alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        got = step()
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_refusals_on_the_device():
     x = torch.zeros((1, 2, 40), device="cuda")
     t = torch.zeros((1, 2), dtype=torch.int32, device="cuda")

@@ -38,7 +38,7 @@ def test_logprobs_refusals(lib):
 
     assert call(dtype=2) == -2 and "dtype" in _err(lib)
     for bad in (dict(B=-1), dict(L=-1), dict(V=0), dict(V=1 << 31, stride=1 << 31), dict(stride=7),
-                dict(T=0.0), dict(T=-1.0), dict(T=math.nan), dict(T=math.inf), dict(nsup=1),
+                dict(T=0.0), dict(T=-1.0), dict(T=math.nan), dict(T=math.inf), dict(T=1e-38), dict(nsup=1),
                 dict(nsup=65), dict(top=33), dict(top=-1), dict(logits=None), dict(targets=None),
                 dict(lp=None), dict(top=1, ids=None), dict(top=1, lps=None), dict(logits=P(257))):
         assert call(**bad) == -1, bad
@@ -126,6 +126,7 @@ def test_attention_refusals(lib):
             assert f(c=_c(**bad)) == status, (f, bad)
         for bad in (dict(B=-1), dict(L=-1), dict(Hq=3), dict(Hq=0), dict(bl=-1), dict(bl=1 << 31),
                     dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf),
+                    dict(scale=2e38),
                     dict(q=None), dict(q=P(257)), dict(lens=None), dict(table=None),
                     dict(stride=1), dict(pages=1 << 26, stride=1 << 26), dict(lse=None)):
             assert f(**bad) == -1, (f, bad)
@@ -184,6 +185,17 @@ def test_binding_refuses_cpu_tensors():
     for bad in (dict(num_pages=0), dict(kv_heads=0), dict(head_dim=96)):
         with pytest.raises(ValueError):
             dc.KVCache(**{**dict(num_pages=1, kv_heads=1, head_dim=64, device="cpu"), **bad})
+
+
+def test_outputs_that_share_memory_are_refused():
+    x = torch.zeros(2, 3, 4, 8)
+    for good in (x, x.transpose(1, 2), x[..., 1:5], x[:, ::2], x[:1].expand(1, 3, 4, 8),
+                 x.permute(3, 2, 1, 0), x[:, :0]):
+        dc._apart(good, "out")
+    for bad in (x[:1].expand(2, 3, 4, 8), x[:, :, :1].expand(2, 3, 4, 8),
+                torch.as_strided(x, (2, 3, 4, 8), (96, 8, 8, 1)), x[..., :1].expand(2, 3, 4, 8)):
+        with pytest.raises(ValueError, match="share memory"):
+            dc._apart(bad, "out")
 
 
 def test_pool_memory_cannot_be_exchanged():
