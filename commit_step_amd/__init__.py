@@ -875,6 +875,7 @@ class KVCache:
         self.device = self._tensors[0].device
         self._c = _CCache(*(t.data_ptr() for t in self._tensors), self.num_pages, self.kv_heads,
                           self.head_dim)
+        self._ref = ctypes.byref(self._c) if self.device.type == "cuda" else None
 
     # the pool's memory cannot be exchanged, only written: the calls hold its addresses
     k = property(lambda self: self._tensors[0], doc="e4m3 codes of the keys (uint8)")
@@ -886,9 +887,9 @@ class KVCache:
 def _cache(cache):
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
-    if cache.device.type != "cuda":
+    if cache._ref is None:
         _dev(cache.k, "cache")
-    return cache.device, ctypes.byref(cache._c)
+    return cache.device, cache._ref
 
 
 def _table(t, name, B, device):
@@ -914,6 +915,11 @@ _Strides = ctypes.c_int64 * 3
 def _heads(t, name, shape, device):
     """A (B, L, heads, head_dim) bfloat16 tensor with unit stride along the last
     dimension; returns its element strides as a C array."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.device == device and \
+            t.shape == shape:
+        sb, sl, sh, sd = t.stride()
+        if sd == 1:
+            return _Strides(sb, sl, sh)
     _dev(t, name)
     if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be a {tuple(shape)} bfloat16 tensor on {device}, not "
@@ -947,7 +953,7 @@ def kv_write(cache, k, v, page_table, start, lens=None):
     dev, c = _cache(cache)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be (B, L, kv_heads, head_dim)")
-    B, L = k.shape[:2]
+    B, L, _, _ = k.shape
     shape = (B, L, cache.kv_heads, cache.head_dim)
     ks = _heads(k, "k", shape, dev)
     vs = _heads(v, "v", shape, dev)
