@@ -105,7 +105,7 @@ struct Share { int b, split, splits, len; };
 
 constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
 
-constexpr int kShareLanes = 8;           // sequences a lane looks after: splits need B <= 512
+constexpr int kShareLanes = 4;           // sequences a lane looks after: splits need B <= 256
 
 // The share in slot `slot`.  Lengths are on the device, so every workgroup works
 // the division out for itself: with `per` pages a share, the smallest (within a
@@ -330,14 +330,16 @@ __device__ __forceinline__ void accumulate(const u32x4 (&vw)[D / 32], const f16x
                                                          tile.o[c], 0, 0, 0);
 }
 
-// Columns' results: the output itself, or this split's part.
+// Columns' results: the output itself (whole: the sequence has one share), or
+// this share's part.
 template <int D>
 __device__ __forceinline__ void store_tile(const AttnArgs &a, int64_t b, int hkv, int64_t c, int slot,
+                                           bool whole,
                                            const Column &col, const Tile<D> &t) {
   const int h = (threadIdx.x & 63) >> 5;
   const float l = halves_sum(t.l);
   if (!col.on) return;
-  if (a.slots == a.B) {
+  if (whole) {
     const float inv = l > 0.f ? 1.0f / l : (l == l ? 0.f : l);
     const int64_t head = (int64_t)hkv * a.G + col.g;
     uint16_t *o = a.out + b * a.os[0] + col.l * a.os[1] + head * a.os[2];
@@ -594,7 +596,7 @@ __global__ __launch_bounds__(64 * CW * KW, D <= 128 ? 2 : 1) void attention_kern
     }
     if (kw_id != 0) return;
   }
-  store_tile<D>(a, b, hkv, c0 + (lane & 31), slot, col, tile);
+  store_tile<D>(a, b, hkv, c0 + (lane & 31), slot, share.splits == 1, col, tile);
 }
 
 // One wave per query and head: joins the shares' parts in their order.  Bound by
@@ -613,6 +615,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
   if (l >= q_len) return;
   const int2 of = a.part_of[b];
+  if (of.y == 1) return;                                  // written already
   const int64_t step = (int64_t)a.H * a.ncols, first = of.x * step + hkv * (int64_t)a.ncols + c;
   const float *ml = a.part_ml + first * 2;
   float m = kNegInf;
@@ -829,16 +832,18 @@ AttnPlan attn_plan(int64_t B, int64_t ncols, int64_t H, int64_t D, int64_t max_p
   const int64_t units = std::max<int64_t>(1, B * H * p.groups);
   p.kw = (D == 256 ? 4 : 8) / p.cw;
   if (p.cw == 4 && units >= 2 * cus) p.kw = 1;
-  // Split the tokens until every CU has its workgroups at once (twice that where
-  // less than two shares a sequence come out of it: then longer sequences can
-  // have more than one), with 2 pages or more per token wave and 4 or more per
-  // share.
-  const int64_t want = (p.cw * p.kw == 8 ? 1 : 2) * cus, rest = H * p.groups;
+  // Split the tokens until every CU has its workgroup, with 2 pages or more per
+  // token wave and 4 or more per share.  Where the sequences come near to that
+  // or do it without, the same number of shares more, for the long ones among
+  // them, if a sequence may have 4 shares or more: 64 sequences of 8 heads, one
+  // of 32768 tokens and the others of 500, take 48 us and not 147; the second
+  // kernel costs batches of equal ones 5 us (64 of 2000: 57, 64 of 500: 29).
+  const int64_t each = cus / (H * p.groups);
   p.min_pages = std::max(2 * p.kw, 4);
-  int64_t s = want / rest;
-  if (s > B && s < 2 * B) s *= 2;
+  int64_t s = each;
+  if (each < 2 * B && max_pages >= 4 * p.min_pages) s = B + each;
   s = std::min({s, B * (max_pages / p.min_pages), B + 127});
-  p.slots = (int)(B > 64 * kShareLanes ? B : std::max(s, B));
+  p.slots = (int)(each < 1 || B > 64 * kShareLanes ? B : std::max(s, B));
   return p;
 }
 
