@@ -845,9 +845,11 @@ def token_logprobs_grad(logits, targets, norm, entropy, grad_logprob, grad_entro
             _same(g, name, torch.float32, (B, L), dev)
     if out is None:
         out = torch.empty((B, L, V), dtype=logits.dtype, device=dev)
-    _dev(out, "out")
-    if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
-        raise ValueError("out must have the logits' dtype, shape and device")
+    else:
+        _dev(out, "out")
+        if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev:
+            raise ValueError("out must have the logits' dtype, shape and device")
+        torch.autograd.graph.increment_version(out)      # a graph that saved it must notice
     return _grad_call(logits, targets, norm, entropy, grad_logprob, grad_entropy, temperature,
                       suppress_ids, out)
 
@@ -1010,11 +1012,14 @@ def block_attention(q, cache, page_table, kv_lens, q_start=None, q_lens=None, bl
     log).  A query that attends to nothing gives 0 and -inf; queries
     l >= q_lens[b] are not written (0 and -inf in outputs allocated here).
     ``weights`` (B, KV_PAGE * pages) float32: every cached token's attention
-    weight, summed over queries and heads, is added to it (see kv_evict).
+    weight, summed over queries and heads, is added to it (see kv_evict).  There
+    is no gradient.
     """
     dev, c = _cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be (B, L, q_heads, head_dim)")
+    if q.requires_grad and torch.is_grad_enabled():
+        raise ValueError("block_attention has no gradient: detach q, or call under no_grad")
     B, L, Hq, D = q.shape
     shape = (B, L, Hq, cache.head_dim)
     qs = _heads(q, "q", shape, dev)

@@ -521,7 +521,8 @@ def test_refusals_on_the_device():
                 dict(weights=torch.zeros((1, 63), device="cuda")), dict(out=q), dict(out=q.float()),
                 dict(lse=torch.zeros((1, 4, 3), device="cuda")), dict(q_lens=ln.cpu()),
                 dict(page_table=_i32([[0, 1, 2, 3]])[:, ::2]),
-                dict(out=torch.zeros_like(q[:, :1]).expand(1, 4, 4, 64))):
+                dict(out=torch.zeros_like(q[:, :1]).expand(1, 4, 4, 64)),
+                dict(q=q.clone().requires_grad_())):
         with pytest.raises(ValueError):
             dc.block_attention(**{**good, **bad})
     w = torch.zeros((1, 64), device="cuda")
@@ -530,6 +531,8 @@ def test_refusals_on_the_device():
         with pytest.raises(ValueError):
             dc.kv_evict(**{**dict(cache=cache, page_table=tb, kv_lens=ln, weights=w, budget=16,
                                   new_pages=_i32([[2]])), **bad})
+    with torch.no_grad():
+        dc.block_attention(**{**good, "q": q.clone().requires_grad_()})
     # empty calls
     r = dc.block_attention(q[:, :0], cache, tb, ln)
     assert r.out.shape == (1, 0, 4, 64) and r.lse.shape == (1, 4, 0)

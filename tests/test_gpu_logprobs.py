@@ -189,6 +189,12 @@ def test_saved_inputs_are_guarded_and_second_order_is_refused():
     y.mul_(2.0)
     with pytest.raises(RuntimeError, match="modified"):
         r.logprob.sum().backward()
+    y = z * 1.0
+    r = dc.token_logprobs(y, t)
+    with torch.no_grad():                              # the gradient written over the logits
+        dc.token_logprobs_grad(y, t, r.norm, r.entropy.detach(), torch.ones((1, 2), device="cuda"), out=y)
+    with pytest.raises(RuntimeError, match="modified"):
+        r.logprob.sum().backward()
 
 
 def test_strided_upstream_gradients_and_unused_outputs():
