@@ -208,6 +208,23 @@ def test_evict_select_long():
         assert np.array_equal(r.kept.cpu().numpy(), kept) and np.array_equal(r.lens.cpu().numpy(), nl)
 
 
+@pytest.mark.parametrize("T", [300, 9000, 33000])
+def test_evict_select_ranges(T):
+    """Weights whose keys take wide, narrow and single ranges, at either end."""
+    rng = np.random.default_rng(T + 1)
+    w = np.stack([1.0 + rng.integers(0, 9, T) * 2.0 ** -23, 3e38 * rng.random(T), rng.random(T) * 1e-44,
+                  np.where(rng.random(T) < 0.01, np.inf, 2.5), np.where(rng.random(T) < 0.5, -np.inf, np.nan),
+                  np.where(np.arange(T) < 3, np.inf, rng.random(T) ** 8), np.full(T, np.inf),
+                  -rng.random(T)]).astype(np.float32)
+    for budget in (7, T // 4, T - 2):
+        for sink, recent in ((0, 0), (4, 3), (budget // 2, budget - budget // 2)):
+            r = dc.evict_select(torch.from_numpy(w).cuda(), _i32([T] * len(w)), budget, sink, recent)
+            kept, nl = okv.evict_select(w, [T] * len(w), budget, sink, recent)
+            assert np.array_equal(r.kept.cpu().numpy(), kept), (budget, sink, recent)
+            want = np.take_along_axis(w, np.maximum(kept, 0).astype(np.int64), 1)
+            assert np.array_equal(r.weights.cpu().numpy(), want, equal_nan=True)
+
+
 # ---------------------------------------------------------------- attention
 
 def _attention_case(seed, B, L, Hq, H, D, T, lens, table=None, scale_q=1.0):
