@@ -62,10 +62,10 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(WriteArgs a) {
   __shared__ __align__(16) uint16_t kt[kPage * ROW], vt[kPage * ROW];
   __shared__ float red[kKvThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t unit = blockIdx.x;
-  const int h = (int)(unit % a.c.H);
-  const int64_t j = unit / a.c.H % a.touched;
-  const int64_t b = unit / a.c.H / a.touched;
+  const uint32_t unit = blockIdx.x / (uint32_t)a.c.H;
+  const int h = (int)(blockIdx.x - unit * (uint32_t)a.c.H);
+  const int64_t b = unit / (uint32_t)a.touched;
+  const int64_t j = unit - (uint32_t)b * (uint32_t)a.touched;
   const int64_t s0 = a.start[b];
   const int64_t n = a.lens ? min((int64_t)a.lens[b], a.L) : a.L;
   if (s0 < 0 || n <= 0) return;
@@ -188,10 +188,10 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(ReadArgs a) {
   constexpr int ROW = D + 2;
   __shared__ __align__(16) uint16_t vt[kPage * ROW];
   const int tid = threadIdx.x;
-  const int64_t unit = blockIdx.x;
-  const int h = (int)(unit % a.c.H);
-  const int64_t p = unit / a.c.H % a.max_pages;
-  const int64_t b = unit / a.c.H / a.max_pages;
+  const uint32_t unit = blockIdx.x / (uint32_t)a.c.H;
+  const int h = (int)(blockIdx.x - unit * (uint32_t)a.c.H);
+  const int64_t b = unit / (uint32_t)a.max_pages;
+  const int64_t p = unit - (uint32_t)b * (uint32_t)a.max_pages;
   const int64_t n = cut_len(a.lens[b], a.max_pages);
   const int64_t page = page_of(a.table + b * a.table_stride, p, a.c.num_pages);
   const int live = page < 0 ? 0 : (int)min(max(n - p * kPage, (int64_t)0), (int64_t)kPage);
@@ -271,10 +271,10 @@ __global__ __launch_bounds__(kKvThreads) void kv_gather_kernel(GatherArgs a) {
   __shared__ int s_ke[kPage], s_ve[kPage];
   __shared__ float red[kKvThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t unit = blockIdx.x;
-  const int h = (int)(unit % a.c.H);
-  const int64_t p = unit / a.c.H % a.new_pages;
-  const int64_t b = unit / a.c.H / a.new_pages;
+  const uint32_t unit = blockIdx.x / (uint32_t)a.c.H;
+  const int h = (int)(blockIdx.x - unit * (uint32_t)a.c.H);
+  const int64_t b = unit / (uint32_t)a.new_pages;
+  const int64_t p = unit - (uint32_t)b * (uint32_t)a.new_pages;
   const int64_t count = min(cut_len(a.counts[b], a.new_pages), a.kept_stride);
   if (p * kPage >= count) return;
   const int64_t page = page_of(a.new_table + b * a.new_stride, p, a.c.num_pages);
