@@ -606,12 +606,14 @@ template <int D>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
-  if (row >= a.B * a.H * a.ncols) return;
-  const int64_t c = row % a.ncols, bh = row / a.ncols;
-  const int hkv = (int)(bh % a.H);
-  const int64_t b = bh / a.H;
-  const int l = (int)(c / a.G), g = (int)(c % a.G);
+  // a call with shares has B <= 256 and few columns: rows fit 32 bits
+  const uint32_t row = __builtin_amdgcn_readfirstlane(blockIdx.x * kJoinWaves + (threadIdx.x >> 6));
+  if (row >= (uint32_t)a.B * a.H * a.ncols) return;
+  const uint32_t bh = row / (uint32_t)a.ncols;
+  const int c = (int)(row - bh * (uint32_t)a.ncols);
+  const int64_t b = bh / (uint32_t)a.H;
+  const int hkv = (int)(bh - (uint32_t)b * a.H);
+  const int l = (int)divide((uint32_t)c, a.by_group), g = c - l * a.G;
   const int64_t q_len = a.q_lens ? min((int64_t)a.q_lens[b], (int64_t)a.L) : a.L;
   if (l >= q_len) return;
   const int2 of = a.part_of[b];
