@@ -5,9 +5,9 @@
 // through LDS.  Bound by HBM bandwidth (a write reads 4 D bytes per token and
 // head and stores 2 D; a read the reverse) and, for a few tokens, by the launch
 // and two dependent fetches.  Measured at 32000 tokens of 8 heads of 128
-// channels: a write 50 us (3.9 TB/s: two sweeps over a page in LDS between load
+// channels: a write 49 us (4.0 TB/s: two sweeps over a page in LDS between load
 // and store, the second after the page's maximum is known), a read 31 us
-// (6.4 TB/s); 8 tokens of 4 heads: 5.5 and 4 us.
+// (6.4 TB/s); 8 tokens of 4 heads: 5.4 and 3.8 us.
 #include <string.h>
 
 #include <algorithm>

@@ -5,8 +5,8 @@
 // candidates for the K largest logits.  Then
 //   log p_t = (x_t - M) / T - log1p(z-),   H = log1p(z-) - ln2 S / (1 + z-).
 // Bound by reading the logits once from HBM: 1024 rows of 151936 bfloat16 with 5
-// alternatives take 69.5 us (4.5 TB/s), 2048 of 126464 without any 111 us
-// (4.7 TB/s); one row, split over 30 workgroups, 14 us with 20 alternatives.
+// alternatives take 69.5 us (4.5 TB/s), 2048 of 126464 without any 108 us
+// (4.8 TB/s); one row, split over 30 workgroups, 14 us with 20 alternatives.
 //
 // Backward, per scored position: p_v from the logits and the forward pass's
 // (M, log z), one read and one write of the row; nothing is summed.  Rows that
