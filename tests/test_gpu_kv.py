@@ -352,6 +352,26 @@ def test_attention_rows_past_q_lens_are_left():
         assert (lse[1] == 7).all() and not (out[0, :2] == 7).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_padded_queries_of_any_bits_add_no_weight(D):
+    """Queries past q_lens and what stands in the caller's lse there do not
+    reach the weights."""
+    cache, ref, table, q, n = _attention_case(3, 3, 40, 4, 2, D, 300, [300, 77, 9])
+    lens, qn = _i32([300, 77, 9]), [33, 1, 0]
+    want = torch.zeros((3, table.shape[1] * PAGE), device="cuda")
+    dc.block_attention(q.cuda(), cache, _i32(table), lens, q_lens=_i32(qn), weights=want)
+    assert torch.isfinite(want).all() and abs(float(want[0].sum()) - 33 * 4) < 1e-2 and not want[2].any()
+    bad = q.cuda().clone()
+    for b in range(3):
+        bad[b, qn[b]:] = float("nan")
+    for bits in (float("nan"), float("inf"), -3e38, 3e38):
+        got = torch.zeros_like(want)
+        lse = torch.full((3, 4, 40), bits, device="cuda")
+        out = torch.full((3, 40, 4, D), 2.0, dtype=torch.bfloat16, device="cuda")
+        dc.block_attention(bad, cache, _i32(table), lens, q_lens=_i32(qn), weights=got, lse=lse, out=out)
+        assert torch.equal(got, want)
+
+
 def test_attention_missing_pages_strides_and_shared_pages():
     T, L, Hq, H, D = 200, 5, 4, 2, 128
     lens = [T, T]
