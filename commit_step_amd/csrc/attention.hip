@@ -730,8 +730,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attention_weights_kerne
   auto step = [&](int u, Cols &x) {
     publish(u + 1);
     __syncthreads();
-    // met nothing, or no query at all (whose lse may be any bits): adds nothing
-    const bool none = x.z == kNegInf || x.lim == 0;
+    // met nothing, a query of NaN or infinities, or no query at all (whose lse may
+    // be any bits): adds nothing
+    const bool none = !bits_finite(__float_as_uint(x.z)) || x.lim == 0;
     const float sub = none ? 0.f : x.z * kLog2e;
     const int lim = none ? 0 : x.lim;
     fetch(u + 2, x);

@@ -584,6 +584,8 @@ size_t dllm_block_attention_workspace_size(int64_t B, int64_t L, int64_t q_heads
 /* dllm_attention_weights: adds to weights[b, t] the attention weight that
  * cached token t received, sum over the queries and query heads of
  * exp(s_t - lse), for the same arguments and the lse of dllm_block_attention.
+ * A query whose lse is not finite (it attends to nothing, or holds NaN or
+ * infinities) adds nothing.
  * weights (B, 32 * max_pages) float32, read and written at t < kv_lens[b]
  * only; each entry is summed in a fixed order.  workspace: at least
  * dllm_attention_weights_workspace_size() bytes, as in dllm_block_attention. */

@@ -444,6 +444,12 @@ def test_nan_query_stays_in_its_row():
     keep = torch.ones((6, 2), dtype=torch.bool)
     keep[2, 1] = False
     assert torch.equal(r.out[0][keep.cuda()], want.out[0][keep.cuda()])
+    # the other queries' weights go on adding up
+    bad[0, 4, 0, 7] = float("inf")
+    w = torch.zeros((1, table.shape[1] * PAGE), device="cuda")
+    r = dc.block_attention(bad.cuda(), cache, _i32(table), _i32([100]), weights=w)
+    assert not torch.isfinite(r.lse[0, 0, 4]) and torch.isfinite(w).all()
+    assert abs(float(w.sum()) - 10) < 1e-3
 
 
 def test_offsets_past_32_bits():
