@@ -837,17 +837,19 @@ AttnPlan attn_plan(int64_t B, int64_t ncols, int64_t H, int64_t D, int64_t max_p
   p.kw = (D == 256 ? 4 : 8) / p.cw;
   if (p.cw == 4 && units >= 2 * cus) p.kw = 1;
   // Split the tokens until every CU has its workgroup, with 2 pages or more per
-  // token wave and 4 or more per share.  Where the sequences come near to that
-  // or do it without, the same number of shares more, for the long ones among
-  // them, if a sequence may have 4 shares or more: 64 sequences of 8 heads, one
-  // of 32768 tokens and the others of 500, take 48 us and not 147; the second
-  // kernel costs batches of equal ones 5 us (64 of 2000: 57, 64 of 500: 29).
-  const int64_t each = cus / (H * p.groups);
+  // token wave and 4 or more per share, where a sequence may have 3 shares:
+  // 2 save less than the second kernel costs (one sequence of 8 heads and 1000
+  // tokens: 13.0 us in 2 shares, 12.3 in one; 2000 tokens: 15.2 in 3, 17.0 in
+  // one).  Where the sequences come near to that number or reach it without, as
+  // many shares more, for the long ones among them, if one may have 4: 64
+  // sequences of 8 heads, one of 32768 tokens and the others of 500, take 48 us
+  // and not 147; batches of equal ones lose 5 us (64 of 2000: 57, 64 of 500: 29).
   p.min_pages = std::max(2 * p.kw, 4);
-  int64_t s = each;
-  if (each < 2 * B && max_pages >= 4 * p.min_pages) s = B + each;
-  s = std::min({s, B * (max_pages / p.min_pages), B + 127});
-  p.slots = (int)(each < 1 || B > 64 * kShareLanes ? B : std::max(s, B));
+  const int64_t each = cus / (H * p.groups), most = max_pages / p.min_pages;
+  int64_t s = B;
+  if (each >= 2 * B && most >= 3) s = std::min(each, B * most);
+  else if (each >= 1 && most >= 4) s = B + each;
+  p.slots = (int)(B > 64 * kShareLanes ? B : std::min(s, B + 127));
   return p;
 }
 
